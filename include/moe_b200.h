@@ -341,6 +341,102 @@ int moe_gemm_fp8_fp4(int M, int N, int K, const uint8_t* A, const uint8_t* A_sca
                      const uint8_t* B_scales, void* out_bf16, void* workspace, size_t workspace_bytes,
                      void* stream);
 
+/* ---- FP8 products with block scales, and the quantiser that feeds them ----------------------
+ *
+ * What a layer next to the experts (projections, a shared expert kept in FP8) computes in training
+ * and serving: activations and weights as 8-bit codes with one scale per block of 128.  A linear
+ * layer y = x W^T with x [T, H], W [N, H] is three products of the one form below:
+ *   forward           y  [T, N] = gemm(A = x,    B = W)       blocks along H
+ *   input gradient    dx [T, H] = gemm(A = dy,   B = W^T)     blocks along N
+ *   weight gradient   dW [N, H] = gemm(A = dy^T, B = x^T)     blocks along T, accumulated in fp32
+ * and moe_quant_fp8 writes each operand and its transposed copy from one reading. */
+
+enum moe_type { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1, MOE_TYPE_FP16 = 2 };
+enum moe_fp8_format { MOE_FP8_E4M3 = 0, MOE_FP8_E5M2 = 1 };
+enum moe_scale_type {
+  MOE_SCALE_FP32 = 0,    /* the scale itself                                  */
+  MOE_SCALE_UE8M0 = 1    /* uint8 code c, scale 2^(c - 127); 255 stands for NaN */
+};
+enum moe_block {
+  MOE_BLOCK_ROW = 0,     /* one scale per row per 128 columns                 */
+  MOE_BLOCK_TILE = 1     /* one scale per 128 rows x 128 columns              */
+};
+
+/* Quantise x [M][K] (x_type, row pitch ldx elements) to FP8 codes and power-of-two scales:
+ *   q   [M][K], row pitch ldq:  blocks of 128 along K (MOE_BLOCK_ROW) or 128 x 128 (MOE_BLOCK_TILE);
+ *       scale of row r (row block r / 128) and K block b at scales[r * s_row_stride + b * s_block_stride]
+ *   qt  [K][M], row pitch ldqt: the transposed copy, blocks of 128 along M or 128 x 128; scale of
+ *       column c (column block) and row block b at scales_t[c * st_row_stride + b * st_block_stride]
+ * either may be NULL (with its scales), not both.  Per block: p = the smallest integer >= -126 with
+ * amax <= MAX * 2^p, MAX = 448 (E4M3) or 57344 (E5M2); p = 0 for an all-zero block; the codes are
+ * x * 2^-p rounded to nearest even, scale = 2^p (UE8M0 code p + 127).  A NaN becomes a NaN code and does
+ * not count towards amax; an infinity gives its block the largest scale, in which it becomes +-MAX and
+ * the finite values of the block zeros or small codes.  The last block of a row or column may be short.
+ * M == 0 or K == 0 writes nothing.  Only the K (M) codes of a row are written, not its padding.
+ * x, 16-byte aligned q and qt with pitches a multiple of 16 (one row: any pitch).  x may not overlap the
+ * outputs.  Asynchronous on `stream`.  MOE_OK, MOE_ERR_INVALID_ARG (pointer, pitch, type),
+ * MOE_ERR_UNSUPPORTED_SHAPE (negative; over 8,388,480 rows with tiles or qt) or MOE_ERR_CUDA. */
+int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_type, int block, int format, int scale_type,
+                  void* q, long long ldq, void* scales, long long s_row_stride, long long s_block_stride, void* qt,
+                  long long ldqt, void* scales_t, long long st_row_stride, long long st_block_stride, void* stream);
+
+/* out[m][n] (+)= sum over K blocks b of  sA(m, b) * sB(n, b) * sum over k in block b of A[m][k] * B[n][k]
+ *
+ * A [M][K] and B [N][K] hold FP8 codes (moe_fp8_format each), row pitches lda, ldb; scales of both are of
+ * scale_type; sA(m, b) = A_scales[(m / a_scale_rows) * as_row_stride + b * as_block_stride] with
+ * a_scale_rows 1 or 128 (likewise B), so any order of the scale arrays is accepted; scales of
+ * consecutive rows next to each other (row stride 1) load fastest.  out [M][N], row pitch ldo, is
+ * bf16 or fp32 (out_type); accumulate (fp32 only) adds to it.  Products and sums are fp32 on the tensor
+ * cores: UE8M0 scales are applied by the block-scaled MMA, fp32 scales (any finite value) to each K
+ * block's fp32 sum outside it.  M, N, K >= 0, odd ones included; K == 0 gives zeros (or adds nothing).
+ * A and B 16-byte aligned, lda and ldb multiples of 16 (one row: any pitch); out aligned to its type (16
+ * bytes and a pitch of a multiple of 16 bytes store fastest); out may not overlap the operands.
+ * `workspace`: 256-byte aligned, at least moe_gemm_fp8_workspace_bytes(), holds the status words in its
+ * first 16 bytes: word 0 is MOE_OK or MOE_ERR_DEVICE_TIMEOUT once the stream reaches the end of the call.
+ * Calls that may overlap on the device need workspaces of their own to tell their status apart.
+ * Asynchronous on `stream`.  MOE_OK, MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE
+ * or MOE_ERR_CUDA. */
+size_t moe_gemm_fp8_workspace_bytes(void);
+int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format, const void* A_scales,
+                 long long as_row_stride, long long as_block_stride, int a_scale_rows, const void* B, long long ldb,
+                 int b_format, const void* B_scales, long long bs_row_stride, long long bs_block_stride,
+                 int b_scale_rows, int scale_type, void* out, long long ldo, int out_type, int accumulate,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Balance loss of the router -----------------------------------------------------------
+ *
+ * The auxiliary loss that moe_update_bias replaces or complements ("전문가 혼합(Mixture of Experts;
+ * MoE)" lesson, "부하 분산 문제"): with scores p[t] = softmax(logits[t]) (MOE_SCORE_SOFTMAX) or
+ * sigmoid(logits[t]) / their sum (MOE_SCORE_SIGMOID), and for sequence s with n_s counted tokens
+ *   counts[s][e] = choices of expert e,   probs[s][e] = mean of p[t][e]  (0 when n_s = 0),
+ *   loss = coef / S' * sum_s E / (k * n_s) * sum_e counts[s][e] * probs[s][e],   S' = sequences with n_s > 0
+ * (0 when there is none); perfectly even routing of every sequence gives coef.
+ * logits [T][E] fp32 or bf16, row pitch ldl; topk_ids int32 [T][k], entries outside [0, E) are not
+ * counted; offsets int32 [S + 1] ascending: sequence s is tokens [offsets[s], offsets[s + 1]), tokens
+ * outside all of them do not count; NULL (then S = 1) = all T tokens; mask uint8 [T], 0 = the token does
+ * not count (its logits are not read); NULL = all count.  A logit of -inf gives a score of 0, a row of
+ * them scores of 0 throughout; NaN and +inf give NaN.  Outputs: loss fp32 [1], counts int32 [S][E], probs
+ * fp32 [S][E], tokens int32 [S] (n_s).  Sums run in fp32 in a fixed order (the loss in fp64): results
+ * repeat bit for bit.  Shapes: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 2^20.
+ * Workspace: 256-byte aligned, moe_balance_workspace_bytes(T, E, S) (0 for an unsupported shape); calls
+ * that may overlap on the device need their own.  Asynchronous on `stream`. */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+size_t moe_balance_workspace_bytes(int T, int E, int S);
+int moe_balance_loss(int T, int E, int k, int S, const void* logits, long long ldl, int logits_type,
+                     const int32_t* topk_ids, const int32_t* offsets, const uint8_t* mask, int score, float coef,
+                     float* loss, int32_t* counts, float* probs, int32_t* tokens, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Gradient of grad_loss[0] * loss with respect to the logits (counts are constants of it), from the counts
+ * and tokens of moe_balance_loss and the same logits, offsets, mask, score, coef and k: grad_logits [T][E]
+ * of the logits' type, row pitch ldg; accumulate adds to it.  Tokens that do not count get zeros (stay as
+ * they were, accumulating).  grad_logits may be the logits' own buffer when not accumulating.  No
+ * workspace.  Asynchronous on `stream`. */
+int moe_balance_loss_backward(int T, int E, int k, int S, const float* grad_loss, const void* logits, long long ldl,
+                              int logits_type, const int32_t* counts, const int32_t* tokens, const int32_t* offsets,
+                              const uint8_t* mask, int score, float coef, void* grad_logits, long long ldg,
+                              int accumulate, void* stream);
+
 /* Release a plan (NULL is a no-op).  Does not free the workspace. */
 void moe_plan_destroy(moe_plan_t plan);
 
