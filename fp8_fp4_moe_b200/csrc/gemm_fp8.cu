@@ -2,21 +2,27 @@
 //
 //   out[m][n] (+)= sum_b sA(m, b) sB(n, b) sum_{k in block b of 128} A[m][k] B[n][k]
 //
-// One operand ("P") is the MMA's 128-row side, the other ("Q") its column side of BN columns.  With many
-// tokens P = A; with few (M <= 128) the roles swap, P = B: the weight rows fill the 128 lanes and BN
-// shrinks to the tokens, so that each weight byte is read once and little is multiplied by padding.
+// One operand ("P") is the MMA's row side, the other ("Q") its column side.  With many tokens P = A; with
+// few (M <= 128) the roles swap, P = B: the weight rows fill the 128 lanes and the columns shrink to the
+// tokens, so that each weight byte is read once and little is multiplied by padding.
 //
-//   warp 0      TMA producer: per 128-deep K block the P tile (128 x 128 B) and the Q tile (BN x 128 B),
-//               128-byte swizzle; codes past the matrix arrive as zeros
+//   warp 0      TMA producer: per 128-deep K block the P tile (128 x 128 B) and the Q tile, 128-byte swizzle;
+//               codes past the matrix arrive as zeros.  fp32 scales: also the scales
 //   warp 1      MMA issuer (one thread)
-//   warps 2..9  epilogue: TMEM lane quarter warp % 4, half of the columns each
-//   warp 10     scales
-// UE8M0 scales (MX): warp 10 writes each stage's scale atoms, tcgen05.mma.kind::mxf8f6f4 applies them and
+//   one warp    (UE8M0 scales) scale atoms
+//   eight warps epilogue: TMEM lane quarter warp % 4, a half of the columns each
+// UE8M0 scales (MX): the scale warp writes each stage's scale atoms, tcgen05.mma.kind::mxf8f6f4 applies them and
 // the accumulator stays in TMEM over the whole K loop.  fp32 scales: each K block is one kind::f8f6f4
 // product into a TMEM buffer of its own, and the epilogue warps add it, scaled, to accumulators in
-// registers while the next block's MMAs run; warp 10 brings the scales in through a ring with cp.async.
-// A tile whose K loop is split over a cluster's CTAs is added up in rank order through distributed
-// shared memory: no workspace, no atomics.
+// registers while the next block's MMAs run; warp 0 brings the scales in through a ring with cp.async.
+// Two kernels:
+//   pair    two CTAs share each M = 256 MMA (cta_group::2), each holding 128 P rows and half of the Q rows.
+//           A single CTA's 128 x 256 tile reads and writes 96 KB of shared memory per K block, 768
+//           clocks at 128 B each for 512 clocks of MMA; in the pair the Q half brings that to 64 KB.
+//           Persistent, up to 256 columns.
+//   small   one CTA per tile of up to 128 columns; where the tiles do not fill the SMs the K loop is split
+//           over the CTAs of a cluster, which add up their parts in rank order through distributed shared
+//           memory: no workspace, no atomics.
 // Every wait is bounded (WaitCtl); on a timeout the CTA records MOE_ERR_DEVICE_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -34,8 +40,10 @@ using namespace moe;
 namespace {
 
 constexpr int BM = 128, BK = 128;
-constexpr int kThreads = 352;                 // TMA, MMA, 8 x epilogue, scales
+constexpr int kPairThreads = 384;             // three warpgroups: TMA, MMA, scale atoms; 2 x epilogue
+constexpr int threads(bool mx) { return mx ? 352 : 320; }   // TMA, MMA, 8 x epilogue (, scale atoms)
 constexpr int kRing = 8;                      // K blocks of fp32 scales in flight
+constexpr int kSfSlots = 2;                   // groups of four K blocks of UE8M0 scales in flight
 constexpr uint32_t kPBytes = BM * BK;
 enum : uint32_t { kWhereProducer = 0xB00, kWhereMma = 0xB10, kWhereEpilogue = 0xB20, kWhereScales = 0xB30,
                   kWhereDrain = 0xB40 };
@@ -43,6 +51,7 @@ enum : uint32_t { kWhereProducer = 0xB00, kWhereMma = 0xB10, kWhereEpilogue = 0x
 struct Fp8Args {
   int p_rows, q_rows, KB;
   int tiles_p, tiles_q, splits;
+  int bn;                            // columns of a tile (pair kernel)
   const void *sp, *sq;               // scales of P and Q
   long sp_row, sp_blk, sq_row, sq_blk;
   int sp_shift, sq_shift;            // 0: per row, 7: per 128 rows
@@ -56,29 +65,50 @@ struct Fp8Args {
 
 template <int BN, bool MX>
 struct Cfg {
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 8 : BN == 32 ? 9 : 10;
+  static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 8 : BN == 32 ? 9 : 10;
   static constexpr int kCols = BN / 2;                           // columns per epilogue thread
-  static constexpr int kAcc = MX ? (BN == 256 ? 1 : 2) : (BN == 256 ? 2 : 4);   // TMEM accumulators
-  static constexpr uint32_t kSfCol = kAcc * BN;                  // MX: scale columns (P 4, Q 4 or 8)
-  static constexpr uint32_t kTmem = (kAcc * BN + (MX ? 12 : 0)) <= 64 ? 64
-                                    : (kAcc * BN + (MX ? 12 : 0)) <= 128 ? 128
-                                    : (kAcc * BN + (MX ? 12 : 0)) <= 256 ? 256 : 512;
+  static constexpr int kAcc = MX ? 2 : 4;                        // TMEM accumulators
+  static constexpr uint32_t kSfCol = kAcc * BN;                  // MX: scale columns (P 4, Q 4; 16 a slot)
+  static constexpr uint32_t kTmem = (kAcc * BN + (MX ? 32 : 0)) <= 64 ? 64
+                                    : (kAcc * BN + (MX ? 32 : 0)) <= 128 ? 128
+                                    : (kAcc * BN + (MX ? 32 : 0)) <= 256 ? 256 : 512;
   static constexpr uint32_t kQBytes = BN * BK;
-  static constexpr uint32_t kSfq = BN > 128 ? 1024 : 512;        // Q scale atoms of a stage
+  static constexpr uint32_t kSfq = 512;                          // Q scale atoms of a slot
   static constexpr uint32_t p = 0;
   static constexpr uint32_t q = p + kStages * kPBytes;
   static constexpr uint32_t sfp = q + kStages * kQBytes;
-  static constexpr uint32_t sfq = sfp + (MX ? kStages * 512 : 0);
-  static constexpr uint32_t ring = sfq + (MX ? kStages * kSfq : 0);
-  static constexpr uint32_t kRingBytes = (BM + BN) * 4;
+  static constexpr uint32_t sfq = sfp + (MX ? kSfSlots * 512 : 0);
+  static constexpr uint32_t ring = sfq + (MX ? kSfSlots * kSfq : 0);
+  static constexpr uint32_t kRingBytes = (BM + (BN < 32 ? 32 : BN)) * 4;   // whole warps write it
   static constexpr uint32_t staging = ring + (MX ? 0 : kRing * kRingBytes);
   static constexpr uint32_t bars = staging + 8 * 2048;
-  static constexpr int kBars = 2 * kStages + 2 * kAcc + 2 * kRing + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kAcc + 2 * kRing + 2 * kSfSlots + 1;
   static constexpr uint32_t misc = bars + kBars * 8;
   static constexpr uint32_t total = misc + 16;
   static constexpr uint32_t bytes = total + 1024;                // 1024-byte alignment of the stages
   static_assert(bytes <= 232448, "shared memory");
-  static_assert(BM * (BN + 0) * 4 + BN * 4 <= sfp, "a partial tile fits over the stages");
+  // a split tile's partial sums [outer][inner + 4], over the stages (inner: the output's contiguous side)
+  static_assert(BM * (BN + 4) * 4 <= sfp && BN * (BM + 4) * 4 <= sfp, "a partial tile fits over the stages");
+};
+
+// The pair kernel: each CTA 128 P rows and half of up to 256 Q rows.
+template <bool MX>
+struct PairCfg {
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kQBytes = 128 * BK;
+  static constexpr uint32_t kSfq = 1024;                         // both CTAs hold the scales of all columns
+  static constexpr uint32_t p = 0;
+  static constexpr uint32_t q = p + kStages * kPBytes;
+  static constexpr uint32_t sfp = q + kStages * kQBytes;
+  static constexpr uint32_t sfq = sfp + (MX ? kSfSlots * 512 : 0);
+  static constexpr uint32_t ring = sfq + (MX ? kSfSlots * kSfq : 0);
+  static constexpr uint32_t kRingBytes = (BM + 256) * 4;
+  static constexpr uint32_t staging = ring + (MX ? 0 : kRing * kRingBytes);
+  static constexpr uint32_t bars = staging + 8 * 2048;
+  static constexpr int kBars = 2 * kStages + 4 + 2 * kRing + 2 * kSfSlots + 1;
+  static constexpr uint32_t misc = bars + kBars * 8;
+  static constexpr uint32_t bytes = misc + 16 + 1024;
+  static_assert(bytes <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ void tc_mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -122,10 +152,74 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool ok) {
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr) : "memory");
   return v;
+}
+// mbar_wait with the abort flag and the clock looked at once in 64 tries: each look costs more than a K block's
+// MMAs, and most waits here end within a few tries.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const WaitCtl& ctl, uint32_t where) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if ((n & 63) != 0) continue;
+    if (*ctl.abort_flag) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > ctl.timeout_ns) {
+      report_status(ctl.status, kStatusTimeout, where, parity);
+      *ctl.abort_flag = 1;
+      __threadfence_block();
+      return false;
+    }
+  }
+  return true;
+}
+// Arrival on the same barrier of CTA 0 of the pair.  No .cluster release: that costs a memory barrier of
+// about 0.7 us, more than a K block's MMAs, and nothing needs it.  An accumulator is handed back with
+// tcgen05.fence, and scale atoms are read by their own SM's async proxy, which the writer's proxy fence
+// has shown them to.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
+
+// One thread of the converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Two fp32 lanes in one register pair (packed FMA halves the instructions of the scaled additions)
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ void tc_mma_f8f6f4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // Tile order: bands of 8 P tiles, every Q tile of a band before the next band, so that what the grid
@@ -145,6 +239,23 @@ __device__ __forceinline__ void put_out(const Fp8Args& p, long m, long n, float 
   } else {
     static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
   }
+}
+
+// four consecutive columns of a row; columns from n_end on are not written
+__device__ __forceinline__ void put_out4(const Fp8Args& p, long m, long n, float4 v, long n_end) {
+  if (p.vec && n + 4 <= n_end && !p.accumulate) {
+    if (p.out_fp32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + m * p.ldo + n) = v;
+    } else {
+      __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + m * p.ldo + n) = *reinterpret_cast<const uint2*>(b);
+    }
+    return;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < n_end) put_out(p, m, n + i, f[i]);
 }
 
 // 64 bytes of each of the warp's 32 rows (lane = row) through the warp's 2 KB buffer, so that stores cover
@@ -191,11 +302,387 @@ __device__ __forceinline__ void store_64b(const Fp8Args& p, uint8_t* buf, const 
   __syncwarp();
 }
 
-// QROW: Q's scales differ by column; otherwise they are one per 128 columns (fp32 scales only).
-template <int BN, bool MX, bool QROW>
-__global__ void __launch_bounds__(kThreads, 1)
-    gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                    const Fp8Args p) {
+// Scale bytes of a tile on their way to the atoms (UE8M0).  An atom's word holds a row's scales of four K
+// blocks of 128; the MMAs of block j take byte j of it for all of their four 32-K steps, so that one copy to
+// TMEM serves four blocks.  Lane l has rows l, l + 32, ... of P (4) and of Q (NR - 4); the bytes of the next
+// four blocks are in flight while the current ones wait for their slot.
+template <int NR>
+struct AtomLoader {
+  long at[NR];                       // offset of the row's scales, -1: past the matrix
+  uint32_t v[NR][4];
+  __device__ __forceinline__ void begin(const Fp8Args& p, int p_row, int q_row, int q_n, int lane) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int in = lane + 32 * (i < 4 ? i : i - 4), row = (i < 4 ? p_row : q_row) + in;
+      const bool live = i < 4 ? row < p.p_rows : in < q_n && row < p.q_rows;
+      at[i] = !live ? -1 : i < 4 ? (long)(row >> p.sp_shift) * p.sp_row : (long)(row >> p.sq_shift) * p.sq_row;
+    }
+  }
+  __device__ __forceinline__ void load(const Fp8Args& p, int kb, int kb1) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const uint8_t* s = static_cast<const uint8_t*>(i < 4 ? p.sp : p.sq) + at[i];
+      const long blk = i < 4 ? p.sp_blk : p.sq_blk;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)    // rows and blocks past the matrix: scale 1
+        v[i][j] = at[i] < 0 || kb + j >= kb1 ? 127u : __ldg(s + (kb + j) * blk);
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* sfp, uint8_t* sfq, int lane) {
+#pragma unroll
+    for (int i = 0; i < NR; i += 4) {
+      uint32_t w[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) w[r] = v[i + r][0] | v[i + r][1] << 8 | v[i + r][2] << 16 | v[i + r][3] << 24;
+      *reinterpret_cast<uint4*>((i < 4 ? sfp : sfq + (i - 4) * 128) + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+};
+// idesc with the scale byte of both operands
+__device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int j) { return idesc | (uint32_t)j << 4 | (uint32_t)j << 29; }
+
+// fp32 scales of one K block into a ring slot: [128] of P, then of Q one per column (QROW) or per 128.
+template <int NQ, bool QROW>
+struct RingLoader {
+  long ap[4], aq[NQ];
+  __device__ __forceinline__ void begin(const Fp8Args& p, int p_row, int q_row, int q_n, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = p_row + lane + 32 * i;
+      ap[i] = row < p.p_rows ? (long)(row >> p.sp_shift) * p.sp_row : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int in = QROW ? lane + 32 * i : lane * 128, row = q_row + in;
+      aq[i] = in < q_n && row < p.q_rows ? (long)(row >> p.sq_shift) * p.sq_row : -1;
+    }
+  }
+  __device__ __forceinline__ void issue(const Fp8Args& p, int kb, float* d, uint64_t* bar, int lane) {
+    const float* sp = static_cast<const float*>(p.sp) + kb * p.sp_blk;
+    const float* sq = static_cast<const float*>(p.sq) + kb * p.sq_blk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cp_async4(d + lane + 32 * i, ap[i] < 0 ? sp : sp + ap[i], ap[i] >= 0);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)     // columns past the tile or the matrix: zeros
+      if (QROW || lane < 2) cp_async4(d + BM + lane + 32 * i, aq[i] < 0 ? sq : sq + aq[i], aq[i] >= 0);
+    cp_async_arrive(bar);
+  }
+};
+
+// ------------------------------------------------------------------ pair kernel
+// QROW (fp32 scales only): Q's scales differ by column; otherwise one per 128 columns, and every tile
+// starts at a multiple of 128.
+template <bool MX, bool QROW>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                         const Fp8Args p) {
+  using C = PairCfg<MX>;
+  constexpr int ST = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // the same offset in both CTAs: dynamic shared memory starts at one address everywhere
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);   // rank 0's count for both
+  uint64_t* empty = full + ST;
+  uint64_t* accf = empty + ST;
+  uint64_t* acce = accf + 2;                                      // rank 0's
+  uint64_t* rfull = acce + 2;
+  uint64_t* rempty = rfull + kRing;
+  uint64_t* sfull = rempty + kRing;                               // rank 0's
+  uint64_t* sempty = sfull + kSfSlots;
+  uint64_t* drain = sempty + kSfSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
+
+  if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);          // rank 0's producer; the bytes of both CTAs
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&accf[i], 1);
+      mbar_init(&acce[i], 16);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&rfull[i], 32);
+      mbar_init(&rempty[i], 8);
+    }
+    for (int i = 0; i < kSfSlots; ++i) {
+      mbar_init(&sfull[i], 2);         // the scale warps of both CTAs
+      mbar_init(&sempty[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();                      // the peer's barriers are initialised before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int KB = p.KB, bn = p.bn;
+  const int tiles = p.tiles_p * p.tiles_q, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  // UE8M0: two accumulators where two of bn columns and the scales behind the first fit, else one
+  const int na = MX && bn > 224 ? 1 : 2;
+  const uint32_t sf_col = bn > 224 ? 256 : 224;
+
+  // fp32 scales: the epilogue warps hold 128 accumulators each, beyond the 168 registers a thread of 12
+  // warps; the first warpgroup gives up what they need: 128 x 72 + 256 x 216 = 384 x 168
+  if (warp < 4) {
+    if constexpr (!MX) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, rphase = 0, fills = 0;
+      const uint32_t q_bytes = (uint32_t)bn / 2 * BK;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        int tp, tq;
+        tile_coord(p, tile, tp, tq);
+        RingLoader<QROW ? 8 : 1, QROW> ring;
+        if constexpr (!MX) ring.begin(p, tp * 256 + rank * BM, tq * bn, bn, lane);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (MX) {
+            if (lane != 0) break;
+            ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer);
+          } else {
+            ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer) &&
+                 wait_for(&rempty[slot], rphase ^ 1, ctl, kWhereScales);
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t fb = mapa_shared(&full[stage], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kPBytes + q_bytes));
+            tma_load_2d_pair(smem + C::p + stage * kPBytes, &tmP, kb * BK, tp * 256 + rank * BM, fb);
+            tma_load_2d_pair(smem + C::q + stage * C::kQBytes, &tmQ, kb * BK, tq * bn + rank * (bn / 2), fb);
+            ++fills;
+          }
+          if constexpr (!MX) {
+            ring.issue(p, kb, reinterpret_cast<float*>(smem + C::ring + slot * C::kRingBytes), &rfull[slot], lane);
+            if (++slot == kRing) { slot = 0; rphase ^= 1; }
+          }
+          if (++stage == ST) { stage = 0; phase ^= 1; }
+        }
+      }
+      if constexpr (!MX) asm volatile("cp.async.wait_all;" ::: "memory");
+      // rank 0's stage barriers count both CTAs' copies: waiting for them covers the peer too
+      if (rank == 0 && lane == 0)
+        for (int s = 0; s < ST; ++s) {
+          const uint32_t n = (fills + ST - 1 - s) / ST;
+          if (n > 0 && !mbar_wait_drain(&full[s], (n - 1) & 1, p.timeout_ns))
+            report_status(p.status, kStatusTimeout, kWhereDrain, s);
+        }
+    } else if (warp == 1) {
+      if (rank == 0) {                 // the whole warp, one elected thread issues: the operands stay uniform
+        const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
+        const uint64_t sp0 = sf_desc(smem_u32(smem + C::sfp)), sq0 = sf_desc(smem_u32(smem + C::sfq));
+        int stage = 0, buf = 0, sf = 0;
+        uint32_t phase = 0, aphase = 0, sphase = 0, tsp = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+          for (int kb = 0; kb < KB; ++kb) {
+            if (!MX || kb == 0) ok = wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma);
+            if (MX && ok && (kb & 3) == 0) ok = wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2);
+            ok = ok && wait_for(&full[stage], phase, ctl, kWhereMma + 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * 256;
+            const uint64_t dp = dp0 + stage * (kPBytes >> 4), dq = dq0 + stage * (C::kQBytes >> 4);
+            if (MX && (kb & 3) == 0) {
+              tsp = tmem + sf_col + sf * 16;     // the slots' columns alternate as well
+              if (elect()) {
+                const uint64_t sp = sp0 + sf * (512 >> 4), sq = sq0 + sf * (C::kSfq >> 4);
+                tc_cp_32x128b_warpx4_pair(tsp, sp);
+                tc_cp_32x128b_warpx4_pair(tsp + 4, sq);
+                tc_cp_32x128b_warpx4_pair(tsp + 8, sq + 32);
+                tc_commit_pair(&sempty[sf], 0x3);
+              }
+              __syncwarp();
+              if (++sf == kSfSlots) { sf = 0; sphase ^= 1; }
+            }
+            if (elect()) {
+              if constexpr (MX) {
+                const uint32_t id = with_byte(p.idesc, kb & 3);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  tc_mma_mxf8f6f4_pair(acc, dp + 2 * i, dq + 2 * i, id, tsp, tsp + 4, kb | i);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc_mma_f8f6f4_pair(acc, dp + 2 * i, dq + 2 * i, p.idesc, i);
+              }
+              tc_commit_pair(&empty[stage], 0x3);
+              if (!MX || kb == KB - 1) tc_commit_pair(&accf[buf], 0x3);
+            }
+            __syncwarp();
+            if (!MX || kb == KB - 1) {
+              if (++buf == na) { buf = 0; aphase ^= 1; }
+            }
+            if (++stage == ST) { stage = 0; phase ^= 1; }
+          }
+        }
+        if (elect()) {
+          tc_commit_pair(drain, 0x1);
+          if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
+        }
+      }
+    } else if (MX && warp == 2) {
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        int tp, tq;
+        tile_coord(p, tile, tp, tq);
+        AtomLoader<12> sf;
+        sf.begin(p, tp * 256 + rank * BM, tq * bn, bn, lane);
+        sf.load(p, 0, KB);
+        for (int kb = 0; kb < KB; kb += 4) {
+          ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
+          if (!ok) break;
+          sf.store(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
+          if (lane == 0) arrive_first(&sfull[slot]);
+          sf.load(p, kb + 4, KB);
+          if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
+        }
+      }
+    }
+  } else {
+    if constexpr (!MX) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ------------------------------------------------------------ epilogue (warps 4..11, both CTAs)
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* obuf = smem + C::staging + (warp - 4) * 2048;
+    // columns [0, h) and [h, bn), h a multiple of 32; both kinds of warp sit on every scheduler
+    const int h = (bn / 2 + 31) & ~31, c0 = half ? h : 0, nc = half ? bn - h : h;
+    const uint32_t t_acc = tmem + c0 + ((uint32_t)(q * 32) << 16);
+    int buf = 0, slot = 0;
+    uint32_t aphase = 0, rphase = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles; tile += step) {
+      int tp, tq;
+      tile_coord(p, tile, tp, tq);
+      uint64_t acc[64];                // two columns each
+      if constexpr (MX) {
+        ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32)
+          if (c < nc) tmem_ld<32>(t_acc + buf * 256 + c, r + c);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(&acce[buf]);
+        if (++buf == na) { buf = 0; aphase ^= 1; }
+#pragma unroll
+        for (int c = 0; c < 64; ++c) acc[c] = pack2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) acc[c] = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = wait_for(&rfull[slot], rphase, ctl, kWhereEpilogue) &&
+               wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float* sc = reinterpret_cast<const float*>(smem + C::ring + slot * C::kRingBytes);
+          const float sp = sc[q * 32 + lane];
+          const uint64_t sp2 = pack2(sp, sp);
+#pragma unroll
+          for (int b = 0; b < 128; b += 64) {    // 64 columns per wait: a load from TMEM takes about 200 clocks
+            if (b < nc) {
+              uint32_t r[64];
+              tmem_ld<32>(t_acc + buf * 256 + b, r);
+              if (b + 32 < nc) tmem_ld<32>(t_acc + buf * 256 + b + 32, r + 32);
+              tmem_ld_wait();
+              if (b + 64 >= nc) {                // everything is read: the buffer may be overwritten
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first(&acce[buf]);
+              }
+              if constexpr (QROW) {
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                  const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(sc + BM + c0 + b + j);
+                  uint64_t& a0 = acc[(b + j) / 2];
+                  uint64_t& a1 = acc[(b + j) / 2 + 1];
+                  a0 = fma2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), mul2(sp2, s4.x), a0);
+                  a1 = fma2(pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), mul2(sp2, s4.y), a1);
+                }
+              } else {
+                // bn is 128 or 256: the 64 columns lie in one block of 128
+                const float s1 = sp * sc[BM + ((c0 + b) >> 7)];
+                const uint64_t s2 = pack2(s1, s1);
+#pragma unroll
+                for (int j = 0; j < 64; j += 2)
+                  acc[(b + j) / 2] = fma2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s2, acc[(b + j) / 2]);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rempty[slot]);
+          if (++buf == 2) { buf = 0; aphase ^= 1; }
+          if (++slot == kRing) { slot = 0; rphase ^= 1; }
+        }
+        if (!ok) break;
+      }
+      const int row = tp * 256 + rank * BM + q * 32, col = tq * bn + c0;   // P row of lane 0, Q row of column 0
+      const int rows = p.p_rows - row;
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        const int cols = min(nc - c, p.q_rows - col - c);
+        if (cols > 0) {
+          uint4 v[4];
+          if (p.out_fp32) {
+#pragma unroll
+            for (int s = 0; s < 32; s += 16) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const ulonglong2 w = make_ulonglong2(acc[(c + s) / 2 + 2 * i], acc[(c + s) / 2 + 2 * i + 1]);
+                v[i] = *reinterpret_cast<const uint4*>(&w);
+              }
+              store_64b(p, obuf, v, row, col + c + s, rows, cols - s, lane);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              __nv_bfloat162 b[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) b[j] = __float22bfloat162_rn(unpack2(acc[c / 2 + 4 * i + j]));
+              v[i] = *reinterpret_cast<const uint4*>(b);
+            }
+            store_64b(p, obuf, v, row, col + c, rows, cols, lane);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();                      // no CTA leaves while its peer may still touch its memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ small kernel
+template <int BN, bool MX>
+__global__ void __launch_bounds__(threads(MX), 1)
+    gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                          const Fp8Args p) {
   using C = Cfg<BN, MX>;
   constexpr int ST = C::kStages, NA = C::kAcc, COLS = C::kCols, CH = COLS < 32 ? COLS : 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -207,7 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acce = accf + NA;
   uint64_t* rfull = acce + NA;
   uint64_t* rempty = rfull + kRing;
-  uint64_t* drain = rempty + kRing;
+  uint64_t* sfull = rempty + kRing;
+  uint64_t* sempty = sfull + kSfSlots;
+  uint64_t* drain = sempty + kSfSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&full[i], MX ? 2 : 1);
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < NA; ++i) {
@@ -226,6 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&rfull[i], 32);
       mbar_init(&rempty[i], 8);
+    }
+    for (int i = 0; i < kSfSlots; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -247,158 +740,113 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kb0 = (int)((long)p.KB * rank / S), kb1 = (int)((long)p.KB * (rank + 1) / S);   // this CTA's K blocks
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, fills = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
-        int tp, tq;
-        tile_coord(p, tile, tp, tq);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, ctl, kWhereProducer)) { ok = false; break; }
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, rphase = 0, fills = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
+      int tp, tq;
+      tile_coord(p, tile, tp, tq);
+      RingLoader<(BN + 31) / 32, true> ring;
+      if constexpr (!MX) ring.begin(p, tp * BM, tq * BN, BN, lane);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (MX) {
+          if (lane != 0) break;
+          ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer);
+        } else {
+          ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer) &&
+               wait_for(&rempty[slot], rphase ^ 1, ctl, kWhereScales);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok) break;
+        if (lane == 0) {
           mbar_arrive_expect_tx(&full[stage], kPBytes + C::kQBytes);
           tma_load_2d(smem + C::p + stage * kPBytes, &tmP, kb * BK, tp * BM, &full[stage]);
           tma_load_2d(smem + C::q + stage * C::kQBytes, &tmQ, kb * BK, tq * BN, &full[stage]);
           ++fills;
-          if (++stage == ST) { stage = 0; phase ^= 1; }
         }
+        if constexpr (!MX) {
+          ring.issue(p, kb, reinterpret_cast<float*>(smem + C::ring + slot * C::kRingBytes), &rfull[slot], lane);
+          if (++slot == kRing) { slot = 0; rphase ^= 1; }
+        }
+        if (++stage == ST) { stage = 0; phase ^= 1; }
       }
-      for (int s = 0; s < ST; ++s) {   // our own copies, before the CTA may exit (they are complete unless aborted)
+    }
+    if constexpr (!MX) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0)
+      for (int s = 0; s < ST; ++s) {   // our own copies, before the CTA may exit (complete unless aborted)
         const uint32_t n = (fills + ST - 1 - s) / ST;
         if (n > 0 && !mbar_wait_drain(&full[s], (n - 1) & 1, p.timeout_ns))
           report_status(p.status, kStatusTimeout, kWhereDrain, s);
       }
-    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if ((!MX || kb == kb0) && !mbar_wait(&acce[buf], aphase ^ 1, ctl, kWhereMma)) { ok = false; break; }
-          if (!mbar_wait(&full[stage], phase, ctl, kWhereMma + 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t acc = tmem + buf * BN;
-          const uint32_t pa = smem_u32(smem + C::p + stage * kPBytes), qa = smem_u32(smem + C::q + stage * C::kQBytes);
+    // the whole warp, one elected thread issues: the operands stay uniform
+    const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
+    const uint64_t sp0 = sf_desc(smem_u32(smem + C::sfp)), sq0 = sf_desc(smem_u32(smem + C::sfq));
+    int stage = 0, buf = 0, sf = 0;
+    uint32_t phase = 0, aphase = 0, sphase = 0, tsp = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int j = (kb - kb0) & 3;
+        if (!MX || kb == kb0) ok = wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma);
+        if (MX && ok && j == 0) ok = wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2);
+        ok = ok && wait_for(&full[stage], phase, ctl, kWhereMma + 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * BN;
+        const uint64_t dp = dp0 + stage * (kPBytes >> 4), dq = dq0 + stage * (C::kQBytes >> 4);
+        if (MX && j == 0) {
+          tsp = tmem + C::kSfCol + sf * 16;      // the slots' columns alternate as well
+          if (elect()) {
+            tc_cp_32x128b_warpx4(tsp, sp0 + sf * (512 >> 4));
+            tc_cp_32x128b_warpx4(tsp + 4, sq0 + sf * (C::kSfq >> 4));
+            tc_commit(&sempty[sf]);
+          }
+          __syncwarp();
+          if (++sf == kSfSlots) { sf = 0; sphase ^= 1; }
+        }
+        if (elect()) {
           if constexpr (MX) {
-            const uint32_t sp = smem_u32(smem + C::sfp + stage * 512), sq = smem_u32(smem + C::sfq + stage * C::kSfq);
-            const uint32_t tsp = tmem + C::kSfCol, tsq = tsp + 4;
-            tc_cp_32x128b_warpx4(tsp, sf_desc(sp));
-            tc_cp_32x128b_warpx4(tsq, sf_desc(sq));
-            if constexpr (BN > 128) tc_cp_32x128b_warpx4(tsq + 4, sf_desc(sq + 512));
+            const uint32_t id = with_byte(p.idesc, j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)   // the four 32-K blocks of a scale share its byte
-              tc_mma_mxf8f6f4(acc, sw128(pa + i * 32), sw128(qa + i * 32), p.idesc, tsp, tsq, (kb > kb0) | i);
+            for (int i = 0; i < 4; ++i) tc_mma_mxf8f6f4(acc, dp + 2 * i, dq + 2 * i, id, tsp, tsp + 4, (kb > kb0) | i);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              tc_mma_f8f6f4(acc, sw128(pa + i * 32), sw128(qa + i * 32), p.idesc, i);
+            for (int i = 0; i < 4; ++i) tc_mma_f8f6f4(acc, dp + 2 * i, dq + 2 * i, p.idesc, i);
           }
           tc_commit(&empty[stage]);
-          if (!MX || kb == kb1 - 1) {
-            tc_commit(&accf[buf]);
-            if (++buf == NA) { buf = 0; aphase ^= 1; }
-          }
-          if (++stage == ST) { stage = 0; phase ^= 1; }
+          if (!MX || kb == kb1 - 1) tc_commit(&accf[buf]);
         }
+        __syncwarp();
+        if (!MX || kb == kb1 - 1) {
+          if (++buf == NA) { buf = 0; aphase ^= 1; }
+        }
+        if (++stage == ST) { stage = 0; phase ^= 1; }
       }
+    }
+    if (elect()) {
       tc_commit(drain);
       if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
     }
-  } else if (warp == 10) {
-    if constexpr (MX) {
-      // scale atoms: lane l writes the words of rows l, l + 32, l + 64, l + 96 (one byte per 32-K block, all
-      // four alike) at l * 16; the bytes of four K blocks are in flight at a time
-      constexpr int NR = BN > 128 ? 12 : 8;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const uint8_t* sp = static_cast<const uint8_t*>(p.sp);
-      const uint8_t* sq = static_cast<const uint8_t*>(p.sq);
-      for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
-        int tp, tq;
-        tile_coord(p, tile, tp, tq);
-        long at[NR];
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const int in = lane + 32 * (i < 4 ? i : i - 4);
-          const int row = (i < 4 ? tp * BM : tq * BN) + in;
-          const bool live = i < 4 ? row < p.p_rows : in < BN && row < p.q_rows;
-          at[i] = !live ? -1 : i < 4 ? (long)(row >> p.sp_shift) * p.sp_row : (long)(row >> p.sq_shift) * p.sq_row;
-        }
-        uint32_t v[4][NR];
-        auto load = [&](int kb, uint32_t (&d)[NR]) {
-#pragma unroll
-          for (int i = 0; i < NR; ++i)   // rows past the matrix: scale 1
-            d[i] = at[i] < 0 || kb >= kb1 ? 127u : i < 4 ? __ldg(sp + at[i] + kb * p.sp_blk) : __ldg(sq + at[i] + kb * p.sq_blk);
-        };
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load(kb0 + j, v[j]);
-        for (int kb = kb0; kb < kb1 && ok; kb += 4) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kb + j < kb1 && ok) {
-              ok = mbar_wait(&empty[stage], phase ^ 1, ctl, kWhereScales);
-              ok = __all_sync(0xffffffffu, ok);
-              if (ok) {
-                constexpr uint32_t kRep = 0x01010101u;
-                *reinterpret_cast<uint4*>(smem + C::sfp + stage * 512 + lane * 16) =
-                    make_uint4(v[j][0] * kRep, v[j][1] * kRep, v[j][2] * kRep, v[j][3] * kRep);
-                *reinterpret_cast<uint4*>(smem + C::sfq + stage * C::kSfq + lane * 16) =
-                    make_uint4(v[j][4] * kRep, v[j][5] * kRep, v[j][6] * kRep, v[j][7] * kRep);
-                if constexpr (BN > 128)
-                  *reinterpret_cast<uint4*>(smem + C::sfq + stage * C::kSfq + 512 + lane * 16) =
-                      make_uint4(v[j][8] * kRep, v[j][9] * kRep, v[j][10] * kRep, v[j][11] * kRep);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[stage]);
-                load(kb + j + 4, v[j]);
-                if (++stage == ST) { stage = 0; phase ^= 1; }
-              }
-            }
-          }
-        }
+  } else if (MX && warp == 10) {
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
+      int tp, tq;
+      tile_coord(p, tile, tp, tq);
+      AtomLoader<8> sf;
+      sf.begin(p, tp * BM, tq * BN, BN, lane);
+      sf.load(p, kb0, kb1);
+      for (int kb = kb0; kb < kb1; kb += 4) {
+        ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
+        if (!ok) break;
+        sf.store(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
+        if (lane == 0) mbar_arrive(&sfull[slot]);
+        sf.load(p, kb + 4, kb1);
+        if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
       }
-    } else {
-      constexpr int NQ = QROW ? (BN + 31) / 32 : 1;
-      int slot = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const float* sp = static_cast<const float*>(p.sp);
-      const float* sq = static_cast<const float*>(p.sq);
-      for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
-        int tp, tq;
-        tile_coord(p, tile, tp, tq);
-        long ap[4], aq[NQ];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = tp * BM + lane + 32 * i;
-          ap[i] = row < p.p_rows ? (long)(row >> p.sp_shift) * p.sp_row : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const int in = QROW ? lane + 32 * i : lane * 128;
-          const int row = tq * BN + in;
-          aq[i] = in < BN && row < p.q_rows ? (long)(row >> p.sq_shift) * p.sq_row : -1;
-        }
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = mbar_wait(&rempty[slot], phase ^ 1, ctl, kWhereScales);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          float* d = reinterpret_cast<float*>(smem + C::ring + slot * C::kRingBytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp_async4(d + lane + 32 * i, ap[i] < 0 ? sp : sp + ap[i] + kb * p.sp_blk, ap[i] >= 0);
-#pragma unroll
-          for (int i = 0; i < NQ; ++i)
-            if (QROW ? lane + 32 * i < BN : lane < BN / 128)
-              cp_async4(d + BM + (QROW ? lane + 32 * i : lane), aq[i] < 0 ? sq : sq + aq[i] + kb * p.sq_blk, aq[i] >= 0);
-          cp_async_arrive(&rfull[slot]);
-          if (++slot == kRing) { slot = 0; phase ^= 1; }
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
@@ -413,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_coord(p, tile, tp, tq);
       float acc[COLS];
       if constexpr (MX) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&accf[buf], aphase, ctl, kWhereEpilogue));
+        ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -428,13 +876,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
         for (int kb = kb0; kb < kb1; ++kb) {
-          ok = mbar_wait(&rfull[slot], rphase, ctl, kWhereEpilogue) && mbar_wait(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
+          ok = wait_for(&rfull[slot], rphase, ctl, kWhereEpilogue) &&
+               wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const float* sc = reinterpret_cast<const float*>(smem + C::ring + slot * C::kRingBytes);
           const float sp = sc[q * 32 + lane];
-          const float spq = QROW ? 0.f : sp * sc[BM + (half * COLS) / 128];
 #pragma unroll
           for (int c = 0; c < COLS; c += CH) {
             uint32_t r[CH];
@@ -445,18 +893,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&acce[buf]);
             }
-            if constexpr (QROW) {
 #pragma unroll
-              for (int j = 0; j < CH; j += 4) {
-                const float4 s4 = *reinterpret_cast<const float4*>(sc + BM + half * COLS + c + j);
-                acc[c + j] += __uint_as_float(r[j]) * (sp * s4.x);
-                acc[c + j + 1] += __uint_as_float(r[j + 1]) * (sp * s4.y);
-                acc[c + j + 2] += __uint_as_float(r[j + 2]) * (sp * s4.z);
-                acc[c + j + 3] += __uint_as_float(r[j + 3]) * (sp * s4.w);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < CH; ++j) acc[c + j] = fmaf(__uint_as_float(r[j]), spq, acc[c + j]);
+            for (int j = 0; j < CH; j += 4) {
+              const float4 s4 = *reinterpret_cast<const float4*>(sc + BM + half * COLS + c + j);
+              acc[c + j] += __uint_as_float(r[j]) * (sp * s4.x);
+              acc[c + j + 1] += __uint_as_float(r[j + 1]) * (sp * s4.y);
+              acc[c + j + 2] += __uint_as_float(r[j + 2]) * (sp * s4.z);
+              acc[c + j + 3] += __uint_as_float(r[j + 3]) * (sp * s4.w);
             }
           }
           __syncwarp();
@@ -469,10 +912,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = tp * BM + q * 32;          // P row of lane 0
       const int col = tq * BN + half * COLS;     // Q row of accumulator column 0
       if (S > 1) {
-        // partial tile [column][129]: rows of a column next to each other, columns on other banks
+        // partial tile in the order of the output: [column][row] swapped, [row][column] otherwise; the pitch
+        // puts neighbouring lanes on other banks
         float* part = reinterpret_cast<float*>(smem);
+        if (p.swap) {
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) part[(half * COLS + c) * (BM + 1) + q * 32 + lane] = acc[c];
+          for (int c = 0; c < COLS; ++c) part[(half * COLS + c) * (BM + 4) + q * 32 + lane] = acc[c];
+        } else {
+#pragma unroll
+          for (int c = 0; c < COLS; c += 4)
+            *reinterpret_cast<float4*>(part + (q * 32 + lane) * (BN + 4) + half * COLS + c) =
+                make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        }
       } else if (p.swap) {
         if (row + lane < p.p_rows) {
 #pragma unroll
@@ -515,23 +966,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 2 && warp < 10) {
       int tp, tq;
       tile_coord(p, blockIdx.x / S, tp, tq);
-      const uint32_t mine = smem_u32(smem);
       uint32_t base[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[r]) : "r"(mine), "r"(r < S ? r : 0));
-      const int t = threadIdx.x - 64;
-      // swapped: this rank's columns, lanes along the rows; otherwise its rows, lanes along the columns
-      const int n_col = p.swap ? BN / S : BN, n_row = p.swap ? BM : BM / S;
-      const int c_base = p.swap ? rank * n_col : 0, r_base = p.swap ? 0 : rank * n_row;
-      for (int i = t; i < n_col * n_row; i += 256) {
-        const int c = c_base + (p.swap ? i / BM : i % BN), r = r_base + (p.swap ? i % BM : i / BN);
-        const int pr = tp * BM + r, qr = tq * BN + c;
-        float v = 0.f;
+      for (int r = 0; r < 8; ++r) base[r] = mapa_shared(smem, r < S ? r : 0);
+      // this rank's share of the tile's outer side (output rows); four consecutive outputs a thread
+      const int inner = p.swap ? BM : BN, outer = (p.swap ? BN : BM) / S;
+      const long m0 = p.swap ? (long)tq * BN : (long)tp * BM, n0 = p.swap ? (long)tp * BM : (long)tq * BN;
+      const int m_end = p.swap ? p.q_rows : p.p_rows, n_end = p.swap ? p.p_rows : p.q_rows;
+      const int quads = inner / 4;
+#pragma unroll 2
+      for (int i = threadIdx.x - 64; i < outer * quads; i += 256) {
+        const int o = rank * outer + i / quads, c = (i % quads) * 4;
+        const uint32_t at = (uint32_t)(o * (inner + 4) + c) * 4;
+        float4 w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (k < S) v += ld_cluster_f32(base[k] + (uint32_t)(c * (BM + 1) + r) * 4);
-        if (pr < p.p_rows && qr < p.q_rows) put_out(p, p.swap ? qr : pr, p.swap ? pr : qr, v);
+          if (k < S) w[k] = ld_cluster_f4(base[k] + at);
+        float4 v = w[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+          if (k < S) {
+            v.x += w[k].x;
+            v.y += w[k].y;
+            v.z += w[k].z;
+            v.w += w[k].w;
+          }
+        if (m0 + o < m_end) put_out4(p, m0 + o, n0 + c, v, n_end);
       }
     }
     __syncwarp();
@@ -547,49 +1007,118 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <int BN, bool MX, bool QROW>
-cudaError_t launch(const CUtensorMap& tp, const CUtensorMap& tq, const Fp8Args& a, int grid, cudaStream_t s) {
-  using C = Cfg<BN, MX>;
-  static std::mutex mu;
-  static bool done[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+using Kernel = void (*)(CUtensorMap, CUtensorMap, Fp8Args);
+struct Launch {
+  Kernel fn;
+  uint32_t smem;
+  int threads, slot;
+};
+
+template <bool MX>
+Launch small_of(int bn) {
+  switch (bn) {
+    case 16: return {gemm_fp8_small_kernel<16, MX>, Cfg<16, MX>::bytes, threads(MX), MX};
+    case 32: return {gemm_fp8_small_kernel<32, MX>, Cfg<32, MX>::bytes, threads(MX), 2 + MX};
+    case 64: return {gemm_fp8_small_kernel<64, MX>, Cfg<64, MX>::bytes, threads(MX), 4 + MX};
+    default: return {gemm_fp8_small_kernel<128, MX>, Cfg<128, MX>::bytes, threads(MX), 6 + MX};
+  }
+}
+Launch pair_of(bool mx, bool qrow) {
+  if (mx) return {gemm_fp8_pair_kernel<true, false>, PairCfg<true>::bytes, kPairThreads, 8};
+  if (qrow) return {gemm_fp8_pair_kernel<false, true>, PairCfg<false>::bytes, kPairThreads, 9};
+  return {gemm_fp8_pair_kernel<false, false>, PairCfg<false>::bytes, kPairThreads, 10};
+}
+
+// The device's SM count, 0 if it is no sm_100, -1 on an error; shared-memory limits raised once.
+constexpr int kMaxDevices = 64;
+std::mutex g_mutex;
+int g_sms[kMaxDevices] = {};
+bool g_ready[kMaxDevices][11] = {};
+
+int device_sms(int* device) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return -1;
+  *device = dev;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (dev < kMaxDevices && g_sms[dev] > 0) return g_sms[dev];
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return -1;
+  if (major != 10 || minor != 0) return 0;
+  if (dev < kMaxDevices) g_sms[dev] = sms;
+  return sms;
+}
+
+cudaError_t launch(const Launch& l, int device, const CUtensorMap& tp, const CUtensorMap& tq, const Fp8Args& a, int grid,
+                   cudaStream_t s) {
   {
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(gemm_fp8_kernel<BN, MX, QROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::bytes);
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (device >= kMaxDevices || !g_ready[device][l.slot]) {
+      const cudaError_t e = cudaFuncSetAttribute(l.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem);
       if (e != cudaSuccess) return e;
-      if (dev < 64) done[dev] = true;
+      if (device < kMaxDevices) g_ready[device][l.slot] = true;
     }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::bytes;
+  cfg.blockDim = dim3(l.threads);
+  cfg.dynamicSmemBytes = l.smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = a.splits;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<BN, MX, QROW>, tp, tq, a);
+  cfg.numAttrs = a.splits > 1 ? 1 : 0;     // the pair kernel carries its own
+  return cudaLaunchKernelEx(&cfg, l.fn, tp, tq, a);
 }
 
-template <bool MX>
-cudaError_t launch_bn(int bn, bool qrow, const CUtensorMap& tp, const CUtensorMap& tq, const Fp8Args& a, int grid,
-                      cudaStream_t s) {
-  if constexpr (!MX) {
-    if (!qrow) return bn == 128 ? launch<128, MX, false>(tp, tq, a, grid, s) : launch<256, MX, false>(tp, tq, a, grid, s);
+// How a product is cut into tiles.
+struct Cut {
+  bool pair, swap;
+  int bn, splits;
+};
+
+int up(long a, long b) { return (int)((a + b - 1) / b); }
+
+Cut choose(int M, int N, int KB, int sms, bool b_tiled, bool mx) {
+  Cut c{false, M <= 128, 128, 1};
+  if (c.swap) {
+    c.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  } else {
+    // columns of a pair tile: the fewest clocks of the busiest pair (2 bn a K block, and about 40 K blocks' worth
+    // of columns for a tile's start and end), wide tiles on a tie
+    const int pairs = sms / 2;
+    long best = -1;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+      if (!mx && b_tiled && bn % 128 != 0) continue;     // one scale per 128 columns: tiles start on them
+      const long waves = up((long)up(M, 256) * up(N, bn), pairs);
+      const long cost = waves * ((long)KB * (bn > 96 ? bn : 96) + 512);
+      if (best < 0 || cost < best) {
+        best = cost;
+        c.bn = bn;
+        c.pair = true;
+      }
+    }
+    // few tiles: the small kernel with the K loop split
+    const long t = (long)up(M, 128) * up(N, 128);
+    if (t * 2 <= sms && KB >= 8) {
+      int s = 1;
+      while (s < 8 && t * s * 2 <= sms && KB >= s * 4) s *= 2;
+      const long cost = (long)up(KB, s) * 192 + 1024;
+      if (cost < best) {
+        c.pair = false;
+        c.bn = 128;
+      }
+    }
   }
-  switch (bn) {
-    case 16: return launch<16, MX, true>(tp, tq, a, grid, s);
-    case 32: return launch<32, MX, true>(tp, tq, a, grid, s);
-    case 64: return launch<64, MX, true>(tp, tq, a, grid, s);
-    case 128: return launch<128, MX, true>(tp, tq, a, grid, s);
-    default: return launch<256, MX, true>(tp, tq, a, grid, s);
+  if (!c.pair) {
+    const long t = (long)up(c.swap ? N : M, 128) * up(c.swap ? M : N, c.bn);
+    while (c.splits < 8 && t * c.splits * 2 <= sms && KB >= c.splits * 4) c.splits *= 2;
   }
+  return c;
 }
 
 }  // namespace
@@ -624,28 +1153,23 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
       (M > 1 && (lda < K || lda % 16)) || (N > 1 && (ldb < K || ldb % 16)) || as_row_stride < 0 ||
       as_block_stride < 0 || bs_row_stride < 0 || bs_block_stride < 0)
     return MOE_ERR_INVALID_ARG;
-  int dev = -1, major = 0, minor = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return MOE_ERR_CUDA;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 0) return MOE_ERR_UNSUPPORTED_SHAPE;   // built for sm_100a only
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((long long)((M + 127) / 128) * ((N + 15) / 16) > (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  int device = 0;
+  const int sms = device_sms(&device);
+  if (sms < 0) return MOE_ERR_CUDA;
+  if (sms == 0) return MOE_ERR_UNSUPPORTED_SHAPE;   // built for sm_100a only
   const bool mx = scale_type == MOE_SCALE_UE8M0;
 
   Fp8Args a{};
-  a.swap = M <= 128;
-  int bn = !a.swap ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  a.KB = (K + 127) / 128;
+  a.KB = up(K, 128);
+  const Cut c = choose(M, N, a.KB, sms, b_scale_rows == 128, mx);
+  a.swap = c.swap;
+  a.splits = c.splits;
+  a.bn = c.bn;
   a.p_rows = a.swap ? N : M;
   a.q_rows = a.swap ? M : N;
-  a.tiles_p = (a.p_rows + 127) / 128;
-  if (!a.swap && (long)a.tiles_p * ((N + 255) / 256) * 4 <= sms) bn = 128;
-  a.tiles_q = (a.q_rows + bn - 1) / bn;
-  if ((long)a.tiles_p * a.tiles_q > (1l << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  const int tiles = a.tiles_p * a.tiles_q;
-  a.splits = 1;
-  while (a.splits < 8 && tiles * a.splits * 2 <= sms && a.KB >= a.splits * 4) a.splits *= 2;
-  const bool qrow = bn < 128 || (a.swap ? a_scale_rows : b_scale_rows) == 1;
+  a.tiles_p = up(a.p_rows, c.pair ? 256 : 128);
+  a.tiles_q = up(a.q_rows, c.bn);
   a.sp = a.swap ? B_scales : A_scales;
   a.sp_row = a.swap ? bs_row_stride : as_row_stride;
   a.sp_blk = a.swap ? bs_block_stride : as_block_stride;
@@ -660,18 +1184,21 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
   a.accumulate = accumulate != 0;
   a.vec = aligned(out, 16) && (M == 1 || ldo * (long long)osize % 16 == 0);
   const uint32_t fp = a.swap ? b_format : a_format, fq = a.swap ? a_format : b_format;
-  a.idesc = mx ? idesc_mxf8f6f4(BM, bn, 0, 0, fp, fq) : idesc_f8f6f4(BM, bn, fp, fq);
+  const int mma_m = c.pair ? 256 : 128;
+  a.idesc = mx ? idesc_mxf8f6f4(mma_m, c.bn, 0, 0, fp, fq) : idesc_f8f6f4(mma_m, c.bn, fp, fq);
   a.status = static_cast<uint32_t*>(workspace);
   a.timeout_ns = 2000000000ull;
 
-  const uint64_t pitch_a = M > 1 ? lda : ((uint64_t)K + 15) / 16 * 16, pitch_b = N > 1 ? ldb : ((uint64_t)K + 15) / 16 * 16;
+  const uint64_t one = ((uint64_t)K + 15) / 16 * 16, pitch_a = M > 1 ? lda : one, pitch_b = N > 1 ? ldb : one;
   CUtensorMap tp, tq;
   if (encode_2d(&tp, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.swap ? B : A, K, a.p_rows, a.swap ? pitch_b : pitch_a, BK, BM) != MOE_OK ||
-      encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.swap ? A : B, K, a.q_rows, a.swap ? pitch_a : pitch_b, BK, bn) != MOE_OK)
+      encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.swap ? A : B, K, a.q_rows, a.swap ? pitch_a : pitch_b, BK,
+                c.pair ? c.bn / 2 : c.bn) != MOE_OK)
     return MOE_ERR_CUDA;
-  const int grid = a.splits > 1 ? tiles * a.splits : tiles < sms ? tiles : sms;
-  const cudaError_t e = mx ? launch_bn<true>(bn, qrow, tp, tq, a, grid, s) : launch_bn<false>(bn, qrow, tp, tq, a, grid, s);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const int tiles = a.tiles_p * a.tiles_q;
+  const int grid = c.pair ? 2 * (tiles < sms / 2 ? tiles : sms / 2) : c.splits > 1 ? tiles * c.splits : tiles < sms ? tiles : sms;
+  const Launch l = c.pair ? pair_of(mx, a.sq_shift == 0) : mx ? small_of<true>(c.bn) : small_of<false>(c.bn);
+  return launch(l, device, tp, tq, a, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
