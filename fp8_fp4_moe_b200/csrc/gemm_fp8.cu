@@ -7,14 +7,14 @@
 // tokens, so that each weight byte is read once and little is multiplied by padding.
 //
 //   warp 0      TMA producer: per 128-deep K block the P tile (128 x 128 B) and the Q tile, 128-byte swizzle;
-//               codes past the matrix arrive as zeros.  fp32 scales: also the scales
-//   warp 1      MMA issuer (one thread)
-//   one warp    (UE8M0 scales) scale atoms
+//               codes past the matrix arrive as zeros
+//   warp 1      MMA issuer
+//   one warp    scales
 //   eight warps epilogue: TMEM lane quarter warp % 4, a half of the columns each
 // UE8M0 scales (MX): the scale warp writes each stage's scale atoms, tcgen05.mma.kind::mxf8f6f4 applies them and
 // the accumulator stays in TMEM over the whole K loop.  fp32 scales: each K block is one kind::f8f6f4
 // product into a TMEM buffer of its own, and the epilogue warps add it, scaled, to accumulators in
-// registers while the next block's MMAs run; warp 0 brings the scales in through a ring with cp.async.
+// registers while the next block's MMAs run.
 // Two kernels:
 //   pair    two CTAs share each M = 256 MMA (cta_group::2), each holding 128 P rows and half of the Q rows.
 //           A single CTA's 128 x 256 tile reads and writes 96 KB of shared memory per K block, 768
@@ -40,10 +40,9 @@ using namespace moe;
 namespace {
 
 constexpr int BM = 128, BK = 128;
-constexpr int kPairThreads = 384;             // three warpgroups: TMA, MMA, scale atoms; 2 x epilogue
-constexpr int threads(bool mx) { return mx ? 352 : 320; }   // TMA, MMA, 8 x epilogue (, scale atoms)
-constexpr int kRing = 8;                      // K blocks of fp32 scales in flight
-constexpr int kSfSlots = 2;                   // groups of four K blocks of UE8M0 scales in flight
+constexpr int kPairThreads = 384;             // three warpgroups: TMA, MMA, scales; 2 x epilogue
+constexpr int kSmallThreads = 352;            // TMA, MMA, 8 x epilogue, scales
+constexpr int kSfSlots = 2;                   // groups of four K blocks whose scales are in flight
 constexpr uint32_t kPBytes = BM * BK;
 enum : uint32_t { kWhereProducer = 0xB00, kWhereMma = 0xB10, kWhereEpilogue = 0xB20, kWhereScales = 0xB30,
                   kWhereDrain = 0xB40 };
@@ -55,6 +54,7 @@ struct Fp8Args {
   const void *sp, *sq;               // scales of P and Q
   long sp_row, sp_blk, sq_row, sq_blk;
   int sp_shift, sq_shift;            // 0: per row, 7: per 128 rows
+  int sp_quad, sq_quad;              // the scales of four K blocks of a row are one aligned load
   void* out;
   long ldo;
   int out_fp32, accumulate, swap, vec;
@@ -79,10 +79,10 @@ struct Cfg {
   static constexpr uint32_t sfp = q + kStages * kQBytes;
   static constexpr uint32_t sfq = sfp + (MX ? kSfSlots * 512 : 0);
   static constexpr uint32_t ring = sfq + (MX ? kSfSlots * kSfq : 0);
-  static constexpr uint32_t kRingBytes = (BM + (BN < 32 ? 32 : BN)) * 4;   // whole warps write it
-  static constexpr uint32_t staging = ring + (MX ? 0 : kRing * kRingBytes);
+  static constexpr uint32_t kRowBytes = (BM + (BN < 32 ? 32 : BN)) * 4;   // fp32 scales of a K block; whole warps write
+  static constexpr uint32_t staging = ring + (MX ? 0 : kSfSlots * 4 * kRowBytes);
   static constexpr uint32_t bars = staging + 8 * 2048;
-  static constexpr int kBars = 2 * kStages + 2 * kAcc + 2 * kRing + 2 * kSfSlots + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kAcc + 2 * kSfSlots + 1;
   static constexpr uint32_t misc = bars + kBars * 8;
   static constexpr uint32_t total = misc + 16;
   static constexpr uint32_t bytes = total + 1024;                // 1024-byte alignment of the stages
@@ -102,10 +102,10 @@ struct PairCfg {
   static constexpr uint32_t sfp = q + kStages * kQBytes;
   static constexpr uint32_t sfq = sfp + (MX ? kSfSlots * 512 : 0);
   static constexpr uint32_t ring = sfq + (MX ? kSfSlots * kSfq : 0);
-  static constexpr uint32_t kRingBytes = (BM + 256) * 4;
-  static constexpr uint32_t staging = ring + (MX ? 0 : kRing * kRingBytes);
+  static constexpr uint32_t kRowBytes = (BM + 256) * 4;            // fp32 scales of a K block
+  static constexpr uint32_t staging = ring + (MX ? 0 : kSfSlots * 4 * kRowBytes);
   static constexpr uint32_t bars = staging + 8 * 2048;
-  static constexpr int kBars = 2 * kStages + 4 + 2 * kRing + 2 * kSfSlots + 1;
+  static constexpr int kBars = 2 * kStages + 8 + 2 * kSfSlots + 1;
   static constexpr uint32_t misc = bars + kBars * 8;
   static constexpr uint32_t bytes = misc + 16 + 1024;
   static_assert(bytes <= 232448, "shared memory");
@@ -143,15 +143,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   }
 }
 
-// 4 bytes global -> shared, zeros when !ok (nothing is read then)
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 4 : 0)
-               : "memory");
+// 16 lanes x 32 columns as matrix fragments: r[4 i + 2 j + e] is TMEM lane 8 j + lane / 4, column
+// 8 i + 2 (lane % 4) + e.  A thread gets 8 columns of several rows instead of all columns of one.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
-// one arrival on `bar` when this thread's copies so far are complete
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
+
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
@@ -176,12 +179,15 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const W
   }
   return true;
 }
-// Arrival on the same barrier of CTA 0 of the pair.  No .cluster release: that costs a memory barrier of
-// about 0.7 us, more than a K block's MMAs, and nothing needs it.  An accumulator is handed back with
-// tcgen05.fence, and scale atoms are read by their own SM's async proxy, which the writer's proxy fence
-// has shown them to.
+// Arrivals on the same barrier of CTA 0 of the pair.  A release at cluster scope costs a memory barrier of
+// about 0.7 us, more than a K block's MMAs.  arrive_first hands scale atoms over: each is read by the async
+// proxy of the SM that wrote it, which the writer's proxy fence has shown it to.  hand_back returns an
+// accumulator: tcgen05.fence::before_thread_sync orders the loads from it, no other memory is passed on.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
+__device__ __forceinline__ void hand_back(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
 
 // One thread of the converged warp.
@@ -190,28 +196,6 @@ __device__ __forceinline__ bool elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// Two fp32 lanes in one register pair (packed FMA halves the instructions of the scaled additions)
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 __device__ __forceinline__ void tc_mma_f8f6f4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                    uint32_t accumulate) {
   asm volatile(
@@ -258,13 +242,14 @@ __device__ __forceinline__ void put_out4(const Fp8Args& p, long m, long n, float
     if (n + i < n_end) put_out(p, m, n + i, f[i]);
 }
 
-// 64 bytes of each of the warp's 32 rows (lane = row) through the warp's 2 KB buffer, so that stores cover
-// whole sectors: 16-byte pieces, 4 lanes to a row, where the row pitch and the columns allow it, else
-// element by element.  row0, col0: first row and column; cols: columns of the matrix from col0 on.
-__device__ __forceinline__ void store_64b(const Fp8Args& p, uint8_t* buf, const uint4 (&v)[4], long row0, long col0,
-                                          int rows, int cols, int lane) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) = v[c];
+// 64 bytes of each of the warp's 32 rows from its 2 KB buffer to global memory, so that stores cover whole
+// sectors: 16-byte pieces, 4 lanes to a row, where the row pitch and the columns allow it, else element by
+// element.  Piece c of row r lies at piece c ^ (r / 2 % 4).  row0, col0: first row and column; cols: columns
+// of the matrix from col0 on.
+__device__ __forceinline__ uint8_t* piece_at(uint8_t* buf, int r, int c) {
+  return buf + r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
+}
+__device__ __forceinline__ void flush_64b(const Fp8Args& p, uint8_t* buf, long row0, long col0, int rows, int cols, int lane) {
   __syncwarp();
   const int esize = p.out_fp32 ? 4 : 2, n = 64 / esize;
   if (p.vec && cols >= n) {
@@ -272,7 +257,7 @@ __device__ __forceinline__ void store_64b(const Fp8Args& p, uint8_t* buf, const 
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int r = it * 8 + (lane >> 2), c = lane & 3;
-      const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
+      const uint4 w = *reinterpret_cast<const uint4*>(piece_at(buf, r, c));
       if (r < rows) {
         uint8_t* d = dst + (long)r * p.ldo * esize + c * 16;
         if (p.accumulate)            // one addition per element and call: the order of them is fixed
@@ -286,7 +271,7 @@ __device__ __forceinline__ void store_64b(const Fp8Args& p, uint8_t* buf, const 
   } else {
     for (int i = lane; i < 32 * n; i += 32) {
       const int r = i / n, c = i - r * n, byte = c * esize;
-      const uint8_t* at = buf + r * 64 + (((byte >> 4) ^ ((r >> 1) & 3)) * 16) + (byte & 15);
+      const uint8_t* at = piece_at(buf, r, byte >> 4) + (byte & 15);
       if (r < rows && c < cols) {
         const long o = (row0 + r) * p.ldo + col0 + c;
         if (p.out_fp32) {
@@ -301,80 +286,135 @@ __device__ __forceinline__ void store_64b(const Fp8Args& p, uint8_t* buf, const 
   }
   __syncwarp();
 }
+// 32 columns of the warp's rows, lane = row
+__device__ __forceinline__ void store_rows(const Fp8Args& p, uint8_t* buf, const float* v, long row0, long col0, int rows,
+                                           int cols, int lane) {
+  if (p.out_fp32) {
+#pragma unroll
+    for (int s = 0; s < 32; s += 16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(piece_at(buf, lane, i)) =
+            make_float4(v[s + 4 * i], v[s + 4 * i + 1], v[s + 4 * i + 2], v[s + 4 * i + 3]);
+      flush_64b(p, buf, row0, col0 + s, rows, cols - s, lane);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+      *reinterpret_cast<uint4*>(piece_at(buf, lane, i)) = *reinterpret_cast<const uint4*>(b);
+    }
+    flush_64b(p, buf, row0, col0, rows, cols, lane);
+  }
+}
+// 32 columns of the warp's rows as fragments (see tmem_ld_frag): v[h * 16 + 4 i + 2 j + e] is row
+// 16 h + 8 j + lane / 4, column 8 i + 2 (lane % 4) + e
+__device__ __forceinline__ void store_frags(const Fp8Args& p, uint8_t* buf, const float* v, long row0, long col0, int rows,
+                                            int cols, int lane) {
+  const int quad = lane & 3, r0 = lane >> 2;
+  if (p.out_fp32) {
+#pragma unroll
+    for (int s = 0; s < 4; s += 2) {           // two groups of 8 columns: 64 bytes
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          *reinterpret_cast<float2*>(piece_at(buf, 8 * h + r0, 2 * i + (quad >> 1)) + (quad & 1) * 8) =
+              make_float2(v[(h >> 1) * 16 + 4 * (s + i) + 2 * (h & 1)], v[(h >> 1) * 16 + 4 * (s + i) + 2 * (h & 1) + 1]);
+      flush_64b(p, buf, row0, col0 + 8 * s, rows, cols - 8 * s, lane);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        *reinterpret_cast<__nv_bfloat162*>(piece_at(buf, 8 * h + r0, i) + quad * 4) =
+            __floats2bfloat162_rn(v[(h >> 1) * 16 + 4 * i + 2 * (h & 1)], v[(h >> 1) * 16 + 4 * i + 2 * (h & 1) + 1]);
+    flush_64b(p, buf, row0, col0, rows, cols, lane);
+  }
+}
 
-// Scale bytes of a tile on their way to the atoms (UE8M0).  An atom's word holds a row's scales of four K
-// blocks of 128; the MMAs of block j take byte j of it for all of their four 32-K steps, so that one copy to
-// TMEM serves four blocks.  Lane l has rows l, l + 32, ... of P (4) and of Q (NR - 4); the bytes of the next
-// four blocks are in flight while the current ones wait for their slot.
-template <int NR>
-struct AtomLoader {
-  long at[NR];                       // offset of the row's scales, -1: past the matrix
+// Scales of a tile on their way into shared memory, four K blocks at a time; rows l, l + 32, l + 64, l + 96
+// of P are lane l's items 0 to 3, its rows of Q the items from 4 on (fp32 with one scale per 128 columns: row
+// 128 l); a warp has the items [FIRST, FIRST + NR).  The next four blocks are in flight
+// while the current ones wait for their slot.
+// UE8M0: an atom's word holds a row's scales of the four blocks; the MMAs of block j take byte j of it for all of
+// their 32-K steps, so that one copy to TMEM serves four blocks.  fp32: per block, [128] of P, then of Q.
+template <bool MX, int FIRST, int NR, bool QROW>
+struct ScaleLoader {
   uint32_t v[NR][4];
-  __device__ __forceinline__ void begin(const Fp8Args& p, int p_row, int q_row, int q_n, int lane) {
+  bool packed[2];                    // MX: v[i][0] is the word already (P, Q)
+  __device__ __forceinline__ void load(const Fp8Args& p, int p_row, int q_row, int q_n, int lane, int kb, int kb1) {
+    constexpr uint32_t kNone = MX ? 127u : 0u;   // past the matrix
+    packed[0] = packed[1] = false;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int in = lane + 32 * (i < 4 ? i : i - 4), row = (i < 4 ? p_row : q_row) + in;
-      const bool live = i < 4 ? row < p.p_rows : in < q_n && row < p.q_rows;
-      at[i] = !live ? -1 : i < 4 ? (long)(row >> p.sp_shift) * p.sp_row : (long)(row >> p.sq_shift) * p.sq_row;
+      const bool is_p = FIRST + i < 4;
+      const int in = is_p ? lane + 32 * (FIRST + i) : QROW ? lane + 32 * (FIRST + i - 4) : lane * 128, row = (is_p ? p_row : q_row) + in;
+      const bool live = is_p ? row < p.p_rows : in < q_n && row < p.q_rows;
+      const long blk = is_p ? p.sp_blk : p.sq_blk;
+      const long at = (is_p ? (long)(row >> p.sp_shift) * p.sp_row : (long)(row >> p.sq_shift) * p.sq_row) + kb * blk;
+      const bool quad = (is_p ? p.sp_quad : p.sq_quad) && kb + 4 <= kb1;
+      if (quad) {
+        if constexpr (MX) {
+          packed[is_p ? 0 : 1] = true;
+          v[i][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_p ? p.sp : p.sq) + at))
+                         : 0x7F7F7F7Fu;
+        } else {
+          const uint4 w = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(is_p ? p.sp : p.sq) + at))
+                               : make_uint4(0, 0, 0, 0);
+          v[i][0] = w.x;
+          v[i][1] = w.y;
+          v[i][2] = w.z;
+          v[i][3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[i][j] = kNone;
+          if (live && kb + j < kb1) {
+            if constexpr (MX)
+              v[i][j] = __ldg(static_cast<const uint8_t*>(is_p ? p.sp : p.sq) + at + j * blk);
+            else
+              v[i][j] = __ldg(static_cast<const uint32_t*>(is_p ? p.sp : p.sq) + at + j * blk);
+          }
+        }
+      }
     }
   }
-  __device__ __forceinline__ void load(const Fp8Args& p, int kb, int kb1) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const uint8_t* s = static_cast<const uint8_t*>(i < 4 ? p.sp : p.sq) + at[i];
-      const long blk = i < 4 ? p.sp_blk : p.sq_blk;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)    // rows and blocks past the matrix: scale 1
-        v[i][j] = at[i] < 0 || kb + j >= kb1 ? 127u : __ldg(s + (kb + j) * blk);
-    }
-  }
-  __device__ __forceinline__ void store(uint8_t* sfp, uint8_t* sfq, int lane) {
+  __device__ __forceinline__ void store_atoms(uint8_t* sfp, uint8_t* sfq, int lane) {
 #pragma unroll
     for (int i = 0; i < NR; i += 4) {
       uint32_t w[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) w[r] = v[i + r][0] | v[i + r][1] << 8 | v[i + r][2] << 16 | v[i + r][3] << 24;
+      for (int r = 0; r < 4; ++r)
+        w[r] = packed[i < 4 ? 0 : 1] ? v[i + r][0] : v[i + r][0] | v[i + r][1] << 8 | v[i + r][2] << 16 | v[i + r][3] << 24;
       *reinterpret_cast<uint4*>((i < 4 ? sfp : sfq + (i - 4) * 128) + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     fence_proxy_async_smem();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void store_rows(uint8_t* slot, uint32_t row_bytes, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t* d = reinterpret_cast<uint32_t*>(slot + j * row_bytes);
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        if (FIRST + i < 4 || QROW || lane < 2) d[lane + 32 * (FIRST + i)] = v[i][j];
+    }
     __syncwarp();
   }
 };
 // idesc with the scale byte of both operands
 __device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int j) { return idesc | (uint32_t)j << 4 | (uint32_t)j << 29; }
 
-// fp32 scales of one K block into a ring slot: [128] of P, then of Q one per column (QROW) or per 128.
-template <int NQ, bool QROW>
-struct RingLoader {
-  long ap[4], aq[NQ];
-  __device__ __forceinline__ void begin(const Fp8Args& p, int p_row, int q_row, int q_n, int lane) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = p_row + lane + 32 * i;
-      ap[i] = row < p.p_rows ? (long)(row >> p.sp_shift) * p.sp_row : -1;
-    }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int in = QROW ? lane + 32 * i : lane * 128, row = q_row + in;
-      aq[i] = in < q_n && row < p.q_rows ? (long)(row >> p.sq_shift) * p.sq_row : -1;
-    }
-  }
-  __device__ __forceinline__ void issue(const Fp8Args& p, int kb, float* d, uint64_t* bar, int lane) {
-    const float* sp = static_cast<const float*>(p.sp) + kb * p.sp_blk;
-    const float* sq = static_cast<const float*>(p.sq) + kb * p.sq_blk;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cp_async4(d + lane + 32 * i, ap[i] < 0 ? sp : sp + ap[i], ap[i] >= 0);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)     // columns past the tile or the matrix: zeros
-      if (QROW || lane < 2) cp_async4(d + BM + lane + 32 * i, aq[i] < 0 ? sq : sq + aq[i], aq[i] >= 0);
-    cp_async_arrive(bar);
-  }
-};
-
 // ------------------------------------------------------------------ pair kernel
 // QROW (fp32 scales only): Q's scales differ by column; otherwise one per 128 columns, and every tile
-// starts at a multiple of 128.
-template <bool MX, bool QROW>
+// starts at a multiple of 128.  NC: columns of an epilogue thread; with fp32 scales bn = 2 NC, known to the
+// compiler so that it can move loads and additions of different columns past each other; UE8M0: up to NC.
+template <bool MX, bool QROW, int NC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                          const Fp8Args p) {
@@ -386,10 +426,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);   // rank 0's count for both
   uint64_t* empty = full + ST;
   uint64_t* accf = empty + ST;
-  uint64_t* acce = accf + 2;                                      // rank 0's
-  uint64_t* rfull = acce + 2;
-  uint64_t* rempty = rfull + kRing;
-  uint64_t* sfull = rempty + kRing;                               // rank 0's
+  uint64_t* acce = accf + 4;                                      // rank 0's
+  uint64_t* sfull = acce + 4;                                     // UE8M0: rank 0's
   uint64_t* sempty = sfull + kSfSlots;
   uint64_t* drain = sempty + kSfSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
@@ -404,17 +442,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&full[i], 1);          // rank 0's producer; the bytes of both CTAs
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&accf[i], 1);
       mbar_init(&acce[i], 16);
     }
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&rfull[i], 32);
-      mbar_init(&rempty[i], 8);
-    }
     for (int i = 0; i < kSfSlots; ++i) {
-      mbar_init(&sfull[i], 2);         // the scale warps of both CTAs
-      mbar_init(&sempty[i], 1);
+      mbar_init(&sfull[i], MX || QROW ? 2 : 1);   // UE8M0: the scale warps of both CTAs; QROW: two warps
+      mbar_init(&sempty[i], MX ? 1 : 8);   // the copies to TMEM, or the epilogue warps
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -432,10 +466,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int KB = p.KB, bn = p.bn;
+  const int KB = p.KB, bn = MX ? p.bn : 2 * NC;
   const int tiles = p.tiles_p * p.tiles_q, first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  // UE8M0: two accumulators where two of bn columns and the scales behind the first fit, else one
-  const int na = MX && bn > 224 ? 1 : 2;
+  // UE8M0: two accumulators where two of bn columns and the scales behind the first fit, else one.  fp32
+  // scales: as many as fit, up to four: from the end of a block's MMAs to the next use of its buffer lie about
+  // 900 clocks of commits, waits and the arrival at the other CTA, which only other buffers' MMAs fill
+  const int na = MX ? (bn > 224 ? 1 : 2) : min(4, 512 / bn);
+  const uint32_t acc_cols = MX ? 256 : bn;
   const uint32_t sf_col = bn > 224 ? 256 : 224;
 
   // fp32 scales: the epilogue warps hold 128 accumulators each, beyond the 168 registers a thread of 12
@@ -443,47 +480,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp < 4) {
     if constexpr (!MX) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, rphase = 0, fills = 0;
-      const uint32_t q_bytes = (uint32_t)bn / 2 * BK;
-      bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += step) {
-        int tp, tq;
-        tile_coord(p, tile, tp, tq);
-        RingLoader<QROW ? 8 : 1, QROW> ring;
-        if constexpr (!MX) ring.begin(p, tp * 256 + rank * BM, tq * bn, bn, lane);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (MX) {
-            if (lane != 0) break;
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0, fills = 0;
+        const uint32_t q_bytes = (uint32_t)bn / 2 * BK, full0 = mapa_shared(full, 0);
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+          int tp, tq;
+          tile_coord(p, tile, tp, tq);
+          for (int kb = 0; kb < KB; ++kb) {
             ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer);
-          } else {
-            ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer) &&
-                 wait_for(&rempty[slot], rphase ^ 1, ctl, kWhereScales);
-            ok = __all_sync(0xffffffffu, ok);
-          }
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t fb = mapa_shared(&full[stage], 0);
+            if (!ok) break;
+            const uint32_t fb = full0 + stage * 8;
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kPBytes + q_bytes));
             tma_load_2d_pair(smem + C::p + stage * kPBytes, &tmP, kb * BK, tp * 256 + rank * BM, fb);
             tma_load_2d_pair(smem + C::q + stage * C::kQBytes, &tmQ, kb * BK, tq * bn + rank * (bn / 2), fb);
             ++fills;
+            if (++stage == ST) { stage = 0; phase ^= 1; }
           }
-          if constexpr (!MX) {
-            ring.issue(p, kb, reinterpret_cast<float*>(smem + C::ring + slot * C::kRingBytes), &rfull[slot], lane);
-            if (++slot == kRing) { slot = 0; rphase ^= 1; }
-          }
-          if (++stage == ST) { stage = 0; phase ^= 1; }
         }
+        // rank 0's stage barriers count both CTAs' copies: waiting for them covers the peer too
+        if (rank == 0)
+          for (int s = 0; s < ST; ++s) {
+            const uint32_t n = (fills + ST - 1 - s) / ST;
+            if (n > 0 && !mbar_wait_drain(&full[s], (n - 1) & 1, p.timeout_ns))
+              report_status(p.status, kStatusTimeout, kWhereDrain, s);
+          }
       }
-      if constexpr (!MX) asm volatile("cp.async.wait_all;" ::: "memory");
-      // rank 0's stage barriers count both CTAs' copies: waiting for them covers the peer too
-      if (rank == 0 && lane == 0)
-        for (int s = 0; s < ST; ++s) {
-          const uint32_t n = (fills + ST - 1 - s) / ST;
-          if (n > 0 && !mbar_wait_drain(&full[s], (n - 1) & 1, p.timeout_ns))
-            report_status(p.status, kStatusTimeout, kWhereDrain, s);
-        }
     } else if (warp == 1) {
       if (rank == 0) {                 // the whole warp, one elected thread issues: the operands stay uniform
         const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
@@ -499,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t acc = tmem + buf * 256;
+            const uint32_t acc = tmem + buf * acc_cols;
             const uint64_t dp = dp0 + stage * (kPBytes >> 4), dq = dq0 + stage * (C::kQBytes >> 4);
             if (MX && (kb & 3) == 0) {
               tsp = tmem + sf_col + sf * 16;     // the slots' columns alternate as well
@@ -538,24 +561,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
         }
       }
-    } else if (MX && warp == 2) {
-      int slot = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += step) {
-        int tp, tq;
-        tile_coord(p, tile, tp, tq);
-        AtomLoader<12> sf;
-        sf.begin(p, tp * 256 + rank * BM, tq * bn, bn, lane);
-        sf.load(p, 0, KB);
-        for (int kb = 0; kb < KB; kb += 4) {
-          ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
-          if (!ok) break;
-          sf.store(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
-          if (lane == 0) arrive_first(&sfull[slot]);
-          sf.load(p, kb + 4, KB);
-          if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
+    } else {
+      auto feed = [&](auto sf) {
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+          int tp, tq;
+          tile_coord(p, tile, tp, tq);
+          const int p_row = tp * 256 + rank * BM, q_row = tq * bn;
+          sf.load(p, p_row, q_row, bn, lane, 0, KB);
+          for (int kb = 0; kb < KB; kb += 4) {
+            ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
+            if (!ok) break;
+            if constexpr (MX) {
+              sf.store_atoms(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
+              if (lane == 0) arrive_first(&sfull[slot]);
+            } else {
+              sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, lane);
+              if (lane == 0) mbar_arrive(&sfull[slot]);
+            }
+            sf.load(p, p_row, q_row, bn, lane, kb + 4, KB);
+            if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
+          }
         }
+      };
+      constexpr int kHalf = (4 + NC / 16) / 2;   // QROW: the items of two warps, which have 72 registers
+      if (warp == 2) {
+        if constexpr (MX)
+          feed(ScaleLoader<true, 0, 12, true>());
+        else if constexpr (QROW)
+          feed(ScaleLoader<false, 0, kHalf, true>());
+        else
+          feed(ScaleLoader<false, 0, 5, false>());
+      } else if constexpr (!MX && QROW) {
+        feed(ScaleLoader<false, kHalf, kHalf, true>());
       }
     }
   } else {
@@ -564,107 +604,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp - 4) >> 2;
     uint8_t* obuf = smem + C::staging + (warp - 4) * 2048;
     // columns [0, h) and [h, bn), h a multiple of 32; both kinds of warp sit on every scheduler
-    const int h = (bn / 2 + 31) & ~31, c0 = half ? h : 0, nc = half ? bn - h : h;
-    const uint32_t t_acc = tmem + c0 + ((uint32_t)(q * 32) << 16);
+    const int h = (bn / 2 + 31) & ~31, c0 = half ? h : 0, nc = MX ? (half ? bn - h : h) : NC;
+    const uint32_t t_acc = tmem + c0 + ((uint32_t)(q * 32) << 16), acce0 = mapa_shared(acce, 0);
     int buf = 0, slot = 0;
     uint32_t aphase = 0, rphase = 0;
     bool ok = true;
     for (int tile = first; tile < tiles; tile += step) {
       int tp, tq;
       tile_coord(p, tile, tp, tq);
-      uint64_t acc[64];                // two columns each
+      float acc[NC];
       if constexpr (MX) {
         ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue));
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[128];
 #pragma unroll
-        for (int c = 0; c < 128; c += 32)
-          if (c < nc) tmem_ld<32>(t_acc + buf * 256 + c, r + c);
+        for (int c = 0; c < NC; c += 32)
+          if (c < nc) tmem_ld<32>(t_acc + buf * acc_cols + c, reinterpret_cast<uint32_t*>(acc + c));
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first(&acce[buf]);
+        if (lane == 0) hand_back(acce0 + buf * 8);
         if (++buf == na) { buf = 0; aphase ^= 1; }
-#pragma unroll
-        for (int c = 0; c < 64; ++c) acc[c] = pack2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
       } else {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) acc[c] = 0;
+        for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+        // 32 columns at a time, the next ones on their way from TMEM while these are added
+        auto load = [&](int c, uint32_t* r) {
+          const uint32_t t = t_acc + buf * acc_cols + c;
+          if constexpr (QROW) {
+            tmem_ld_frag(t, r);
+            tmem_ld_frag(t + (16u << 16), r + 16);
+          } else {
+            tmem_ld<32>(t, r);
+          }
+        };
         for (int kb = 0; kb < KB; ++kb) {
-          ok = wait_for(&rfull[slot], rphase, ctl, kWhereEpilogue) &&
-               wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
+          const int j4 = kb & 3;
+          if (j4 == 0) ok = wait_for(&sfull[slot], rphase, ctl, kWhereEpilogue);
+          const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + j4) * C::kRowBytes);
+          float sp[QROW ? 4 : 1];
+          if constexpr (QROW) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) sp[h] = sc[q * 32 + 8 * h + (lane >> 2)];
+          } else {
+            sp[0] = sc[q * 32 + lane] * sc[BM + (c0 >> 7)];   // bn is 128 or 256: one block of 128 columns
+          }
+          ok = ok && wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const float* sc = reinterpret_cast<const float*>(smem + C::ring + slot * C::kRingBytes);
-          const float sp = sc[q * 32 + lane];
-          const uint64_t sp2 = pack2(sp, sp);
+          uint32_t r[2][32];
+          load(0, r[0]);
+          tmem_ld_wait();
 #pragma unroll
-          for (int b = 0; b < 128; b += 64) {    // 64 columns per wait: a load from TMEM takes about 200 clocks
-            if (b < nc) {
-              uint32_t r[64];
-              tmem_ld<32>(t_acc + buf * 256 + b, r);
-              if (b + 32 < nc) tmem_ld<32>(t_acc + buf * 256 + b + 32, r + 32);
-              tmem_ld_wait();
-              if (b + 64 >= nc) {                // everything is read: the buffer may be overwritten
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_first(&acce[buf]);
-              }
-              if constexpr (QROW) {
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                  const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(sc + BM + c0 + b + j);
-                  uint64_t& a0 = acc[(b + j) / 2];
-                  uint64_t& a1 = acc[(b + j) / 2 + 1];
-                  a0 = fma2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), mul2(sp2, s4.x), a0);
-                  a1 = fma2(pack2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), mul2(sp2, s4.y), a1);
-                }
-              } else {
-                // bn is 128 or 256: the 64 columns lie in one block of 128
-                const float s1 = sp * sc[BM + ((c0 + b) >> 7)];
-                const uint64_t s2 = pack2(s1, s1);
-#pragma unroll
-                for (int j = 0; j < 64; j += 2)
-                  acc[(b + j) / 2] = fma2(pack2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s2, acc[(b + j) / 2]);
-              }
+          for (int i = 0; i < NC / 32; ++i) {
+            if (i + 1 < NC / 32) {
+              load((i + 1) * 32, r[(i + 1) & 1]);
+            } else {                             // everything is read: the buffer may be overwritten
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) hand_back(acce0 + buf * 8);
             }
+            const uint32_t(&v)[32] = r[i & 1];
+            float* a = acc + i * 32;
+            if constexpr (QROW) {
+              // 8 bytes of column scales serve four rows: with a row to a lane, every lane would read all
+              // columns' scales, and shared memory returns 128 bytes a clock whether they differ or not
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 sq = *reinterpret_cast<const float2*>(sc + BM + c0 + i * 32 + 8 * j + 2 * (lane & 3));
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  const int e = (h >> 1) * 16 + 4 * j + 2 * (h & 1);
+                  a[e] = fmaf(__uint_as_float(v[e]), sp[h] * sq.x, a[e]);
+                  a[e + 1] = fmaf(__uint_as_float(v[e + 1]), sp[h] * sq.y, a[e + 1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) a[j] = fmaf(__uint_as_float(v[j]), sp[0], a[j]);
+            }
+            if (i + 1 < NC / 32) tmem_ld_wait();
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rempty[slot]);
-          if (++buf == 2) { buf = 0; aphase ^= 1; }
-          if (++slot == kRing) { slot = 0; rphase ^= 1; }
+          if (++buf == na) { buf = 0; aphase ^= 1; }
+          if (j4 == 3 || kb == KB - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[slot]);
+            if (++slot == kSfSlots) { slot = 0; rphase ^= 1; }
+          }
         }
         if (!ok) break;
       }
       const int row = tp * 256 + rank * BM + q * 32, col = tq * bn + c0;   // P row of lane 0, Q row of column 0
       const int rows = p.p_rows - row;
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < NC; c += 32) {
         const int cols = min(nc - c, p.q_rows - col - c);
         if (cols > 0) {
-          uint4 v[4];
-          if (p.out_fp32) {
-#pragma unroll
-            for (int s = 0; s < 32; s += 16) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const ulonglong2 w = make_ulonglong2(acc[(c + s) / 2 + 2 * i], acc[(c + s) / 2 + 2 * i + 1]);
-                v[i] = *reinterpret_cast<const uint4*>(&w);
-              }
-              store_64b(p, obuf, v, row, col + c + s, rows, cols - s, lane);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              __nv_bfloat162 b[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) b[j] = __float22bfloat162_rn(unpack2(acc[c / 2 + 4 * i + j]));
-              v[i] = *reinterpret_cast<const uint4*>(b);
-            }
-            store_64b(p, obuf, v, row, col + c, rows, cols, lane);
-          }
+          if constexpr (!MX && QROW)
+            store_frags(p, obuf, acc + c, row, col + c, rows, cols, lane);
+          else
+            store_rows(p, obuf, acc + c, row, col + c, rows, cols, lane);
         }
       }
     }
@@ -680,7 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------------ small kernel
 template <int BN, bool MX>
-__global__ void __launch_bounds__(threads(MX), 1)
+__global__ void __launch_bounds__(kSmallThreads, 1)
     gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                           const Fp8Args p) {
   using C = Cfg<BN, MX>;
@@ -692,9 +732,7 @@ __global__ void __launch_bounds__(threads(MX), 1)
   uint64_t* empty = full + ST;
   uint64_t* accf = empty + ST;
   uint64_t* acce = accf + NA;
-  uint64_t* rfull = acce + NA;
-  uint64_t* rempty = rfull + kRing;
-  uint64_t* sfull = rempty + kRing;
+  uint64_t* sfull = acce + NA;
   uint64_t* sempty = sfull + kSfSlots;
   uint64_t* drain = sempty + kSfSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
@@ -712,13 +750,9 @@ __global__ void __launch_bounds__(threads(MX), 1)
       mbar_init(&accf[i], 1);
       mbar_init(&acce[i], 8);
     }
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&rfull[i], 32);
-      mbar_init(&rempty[i], 8);
-    }
     for (int i = 0; i < kSfSlots; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&sempty[i], 1);
+      mbar_init(&sempty[i], MX ? 1 : 8);   // the copies to TMEM, or the epilogue warps
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -737,47 +771,34 @@ __global__ void __launch_bounds__(threads(MX), 1)
 
   const int S = p.splits, rank = blockIdx.x % S;
   const int tiles = p.tiles_p * p.tiles_q, step = gridDim.x / S;
-  const int kb0 = (int)((long)p.KB * rank / S), kb1 = (int)((long)p.KB * (rank + 1) / S);   // this CTA's K blocks
+  // this CTA's K blocks: whole groups of four, whose scales load together
+  const int groups = (p.KB + 3) / 4;
+  const int kb0 = groups * rank / S * 4, kb1 = min(p.KB, groups * (rank + 1) / S * 4);
 
   if (warp == 0) {
-    int stage = 0, slot = 0;
-    uint32_t phase = 0, rphase = 0, fills = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
-      int tp, tq;
-      tile_coord(p, tile, tp, tq);
-      RingLoader<(BN + 31) / 32, true> ring;
-      if constexpr (!MX) ring.begin(p, tp * BM, tq * BN, BN, lane);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (MX) {
-          if (lane != 0) break;
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, fills = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
+        int tp, tq;
+        tile_coord(p, tile, tp, tq);
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer);
-        } else {
-          ok = wait_for(&empty[stage], phase ^ 1, ctl, kWhereProducer) &&
-               wait_for(&rempty[slot], rphase ^ 1, ctl, kWhereScales);
-          ok = __all_sync(0xffffffffu, ok);
-        }
-        if (!ok) break;
-        if (lane == 0) {
+          if (!ok) break;
           mbar_arrive_expect_tx(&full[stage], kPBytes + C::kQBytes);
           tma_load_2d(smem + C::p + stage * kPBytes, &tmP, kb * BK, tp * BM, &full[stage]);
           tma_load_2d(smem + C::q + stage * C::kQBytes, &tmQ, kb * BK, tq * BN, &full[stage]);
           ++fills;
+          if (++stage == ST) { stage = 0; phase ^= 1; }
         }
-        if constexpr (!MX) {
-          ring.issue(p, kb, reinterpret_cast<float*>(smem + C::ring + slot * C::kRingBytes), &rfull[slot], lane);
-          if (++slot == kRing) { slot = 0; rphase ^= 1; }
-        }
-        if (++stage == ST) { stage = 0; phase ^= 1; }
       }
-    }
-    if constexpr (!MX) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0)
       for (int s = 0; s < ST; ++s) {   // our own copies, before the CTA may exit (complete unless aborted)
         const uint32_t n = (fills + ST - 1 - s) / ST;
         if (n > 0 && !mbar_wait_drain(&full[s], (n - 1) & 1, p.timeout_ns))
           report_status(p.status, kStatusTimeout, kWhereDrain, s);
       }
+    }
   } else if (warp == 1) {
     // the whole warp, one elected thread issues: the operands stay uniform
     const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
@@ -829,22 +850,24 @@ __global__ void __launch_bounds__(threads(MX), 1)
       tc_commit(drain);
       if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
     }
-  } else if (MX && warp == 10) {
+  } else if (warp == 10) {
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
       int tp, tq;
       tile_coord(p, tile, tp, tq);
-      AtomLoader<8> sf;
-      sf.begin(p, tp * BM, tq * BN, BN, lane);
-      sf.load(p, kb0, kb1);
+      ScaleLoader<MX, 0, MX ? 8 : 4 + (BN + 31) / 32, true> sf;
+      sf.load(p, tp * BM, tq * BN, BN, lane, kb0, kb1);
       for (int kb = kb0; kb < kb1; kb += 4) {
         ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
         if (!ok) break;
-        sf.store(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
+        if constexpr (MX)
+          sf.store_atoms(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
+        else
+          sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, lane);
         if (lane == 0) mbar_arrive(&sfull[slot]);
-        sf.load(p, kb + 4, kb1);
+        sf.load(p, tp * BM, tq * BN, BN, lane, kb + 4, kb1);
         if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
       }
     }
@@ -876,12 +899,13 @@ __global__ void __launch_bounds__(threads(MX), 1)
 #pragma unroll
         for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
         for (int kb = kb0; kb < kb1; ++kb) {
-          ok = wait_for(&rfull[slot], rphase, ctl, kWhereEpilogue) &&
-               wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
+          const int j4 = (kb - kb0) & 3;
+          if (j4 == 0) ok = wait_for(&sfull[slot], rphase, ctl, kWhereEpilogue);
+          ok = ok && wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          const float* sc = reinterpret_cast<const float*>(smem + C::ring + slot * C::kRingBytes);
+          const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + j4) * C::kRowBytes);
           const float sp = sc[q * 32 + lane];
 #pragma unroll
           for (int c = 0; c < COLS; c += CH) {
@@ -902,10 +926,12 @@ __global__ void __launch_bounds__(threads(MX), 1)
               acc[c + j + 3] += __uint_as_float(r[j + 3]) * (sp * s4.w);
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rempty[slot]);
           if (++buf == NA) { buf = 0; aphase ^= 1; }
-          if (++slot == kRing) { slot = 0; rphase ^= 1; }
+          if (j4 == 3 || kb == kb1 - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[slot]);
+            if (++slot == kSfSlots) { slot = 0; rphase ^= 1; }
+          }
         }
         if (!ok) break;
       }
@@ -933,30 +959,8 @@ __global__ void __launch_bounds__(threads(MX), 1)
       } else if constexpr (COLS >= 32) {
         const int rows = p.p_rows - row;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
-          if (col + c < p.q_rows) {
-            uint4 v[4];
-            if (p.out_fp32) {
-#pragma unroll
-              for (int h = 0; h < 32; h += 16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  v[i] = make_uint4(__float_as_uint(acc[c + h + 4 * i]), __float_as_uint(acc[c + h + 4 * i + 1]),
-                                    __float_as_uint(acc[c + h + 4 * i + 2]), __float_as_uint(acc[c + h + 4 * i + 3]));
-                store_64b(p, obuf, v, row, col + c + h, rows, p.q_rows - col - c - h, lane);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                __nv_bfloat162 b[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(acc[c + 8 * i + 2 * j], acc[c + 8 * i + 2 * j + 1]);
-                v[i] = *reinterpret_cast<const uint4*>(b);
-              }
-              store_64b(p, obuf, v, row, col + c, rows, p.q_rows - col - c, lane);
-            }
-          }
-        }
+        for (int c = 0; c < COLS; c += 32)
+          if (col + c < p.q_rows) store_rows(p, obuf, acc + c, row, col + c, rows, p.q_rows - col - c, lane);
       }
     }
   }
@@ -1017,23 +1021,26 @@ struct Launch {
 template <bool MX>
 Launch small_of(int bn) {
   switch (bn) {
-    case 16: return {gemm_fp8_small_kernel<16, MX>, Cfg<16, MX>::bytes, threads(MX), MX};
-    case 32: return {gemm_fp8_small_kernel<32, MX>, Cfg<32, MX>::bytes, threads(MX), 2 + MX};
-    case 64: return {gemm_fp8_small_kernel<64, MX>, Cfg<64, MX>::bytes, threads(MX), 4 + MX};
-    default: return {gemm_fp8_small_kernel<128, MX>, Cfg<128, MX>::bytes, threads(MX), 6 + MX};
+    case 16: return {gemm_fp8_small_kernel<16, MX>, Cfg<16, MX>::bytes, kSmallThreads, MX};
+    case 32: return {gemm_fp8_small_kernel<32, MX>, Cfg<32, MX>::bytes, kSmallThreads, 2 + MX};
+    case 64: return {gemm_fp8_small_kernel<64, MX>, Cfg<64, MX>::bytes, kSmallThreads, 4 + MX};
+    default: return {gemm_fp8_small_kernel<128, MX>, Cfg<128, MX>::bytes, kSmallThreads, 6 + MX};
   }
 }
-Launch pair_of(bool mx, bool qrow) {
-  if (mx) return {gemm_fp8_pair_kernel<true, false>, PairCfg<true>::bytes, kPairThreads, 8};
-  if (qrow) return {gemm_fp8_pair_kernel<false, true>, PairCfg<false>::bytes, kPairThreads, 9};
-  return {gemm_fp8_pair_kernel<false, false>, PairCfg<false>::bytes, kPairThreads, 10};
+Launch pair_of(bool mx, bool qrow, int bn) {
+  if (mx) return {gemm_fp8_pair_kernel<true, false, 128>, PairCfg<true>::bytes, kPairThreads, 8};
+  if (bn == 256)
+    return qrow ? Launch{gemm_fp8_pair_kernel<false, true, 128>, PairCfg<false>::bytes, kPairThreads, 9}
+                : Launch{gemm_fp8_pair_kernel<false, false, 128>, PairCfg<false>::bytes, kPairThreads, 10};
+  return qrow ? Launch{gemm_fp8_pair_kernel<false, true, 64>, PairCfg<false>::bytes, kPairThreads, 11}
+              : Launch{gemm_fp8_pair_kernel<false, false, 64>, PairCfg<false>::bytes, kPairThreads, 12};
 }
 
 // The device's SM count, 0 if it is no sm_100, -1 on an error; shared-memory limits raised once.
 constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices] = {};
-bool g_ready[kMaxDevices][11] = {};
+bool g_ready[kMaxDevices][13] = {};
 
 int device_sms(int* device) {
   int dev = -1;
@@ -1093,7 +1100,7 @@ Cut choose(int M, int N, int KB, int sms, bool b_tiled, bool mx) {
     const int pairs = sms / 2;
     long best = -1;
     for (int bn = 256; bn >= 64; bn -= 32) {
-      if (!mx && b_tiled && bn % 128 != 0) continue;     // one scale per 128 columns: tiles start on them
+      if (!mx && bn != 256 && bn != 128) continue;       // the widths compiled for fp32 scales
       const long waves = up((long)up(M, 256) * up(N, bn), pairs);
       const long cost = waves * ((long)KB * (bn > 96 ? bn : 96) + 512);
       if (best < 0 || cost < best) {
@@ -1106,7 +1113,7 @@ Cut choose(int M, int N, int KB, int sms, bool b_tiled, bool mx) {
     const long t = (long)up(M, 128) * up(N, 128);
     if (t * 2 <= sms && KB >= 8) {
       int s = 1;
-      while (s < 8 && t * s * 2 <= sms && KB >= s * 4) s *= 2;
+      while (s < 8 && t * s * 2 <= sms && KB >= s * 8) s *= 2;
       const long cost = (long)up(KB, s) * 192 + 1024;
       if (cost < best) {
         c.pair = false;
@@ -1116,7 +1123,7 @@ Cut choose(int M, int N, int KB, int sms, bool b_tiled, bool mx) {
   }
   if (!c.pair) {
     const long t = (long)up(c.swap ? N : M, 128) * up(c.swap ? M : N, c.bn);
-    while (c.splits < 8 && t * c.splits * 2 <= sms && KB >= c.splits * 4) c.splits *= 2;
+    while (c.splits < 8 && t * c.splits * 2 <= sms && KB >= c.splits * 8) c.splits *= 2;   // a group of 4 or more each
   }
   return c;
 }
@@ -1178,6 +1185,9 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
   a.sq_row = a.swap ? as_row_stride : bs_row_stride;
   a.sq_blk = a.swap ? as_block_stride : bs_block_stride;
   a.sq_shift = (a.swap ? a_scale_rows : b_scale_rows) == 128 ? 7 : 0;
+  const uintptr_t quad = 4 * ssize;
+  a.sp_quad = a.sp_blk == 1 && a.sp_row % 4 == 0 && aligned(a.sp, quad);
+  a.sq_quad = a.sq_blk == 1 && a.sq_row % 4 == 0 && aligned(a.sq, quad);
   a.out = out;
   a.ldo = M > 1 ? ldo : N;
   a.out_fp32 = f32;
@@ -1197,7 +1207,7 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
     return MOE_ERR_CUDA;
   const int tiles = a.tiles_p * a.tiles_q;
   const int grid = c.pair ? 2 * (tiles < sms / 2 ? tiles : sms / 2) : c.splits > 1 ? tiles * c.splits : tiles < sms ? tiles : sms;
-  const Launch l = c.pair ? pair_of(mx, a.sq_shift == 0) : mx ? small_of<true>(c.bn) : small_of<false>(c.bn);
+  const Launch l = c.pair ? pair_of(mx, a.sq_shift == 0, c.bn) : mx ? small_of<true>(c.bn) : small_of<false>(c.bn);
   return launch(l, device, tp, tq, a, grid, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -84,6 +84,23 @@ def test_exact_formats_and_scale_blocks(cuda_lib, M, N, K, kind, a_per, fa, fb):
     _equal(*binding.gemm_fp8(*op, out_dtype=torch.float32), ref)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 300, 3584), (20, 128, 3600), (64, 512, 7168), (128, 200, 2049), (300, 256, 1537)])
+@pytest.mark.parametrize("kind", ["fp32", "ue8m0"])
+@pytest.mark.parametrize("order", ["rows", "columns"])
+def test_exact_long_k(cuda_lib, M, N, K, kind, order):
+    # K loops split over CTAs at block counts that are and are not multiples of four, scales of a row or of a column
+    # next to each other; codes of -1, 0 and 1, so that the sums stay below 7168 * 25 (fp32) and 7168 * 16 units
+    rng = np.random.default_rng(K)
+    a, A = _codes(rng, M, K, "e4m3")
+    b, B = _codes(rng, N, K, "e4m3")
+    for v, t in ((a, A), (b, B)):
+        np.sign(v, out=v)
+        t.view(torch.uint8).copy_(torch.from_numpy(O.encode_fp8(v, "e4m3")))
+    sa, As = _scales(rng, M, K, "row", kind, order)
+    sb, Bs = _scales(rng, N, K, "tile", kind, order)
+    _equal(*binding.gemm_fp8(A, As, B, Bs, out_dtype=torch.float32), O.gemm(a, sa, b, sb)[0])
+
+
 @pytest.mark.parametrize("M,N,K", [(9, 200, 300), (129, 260, 1024), (700, 513, 128)])
 @pytest.mark.parametrize("kind", ["fp32", "ue8m0"])
 def test_accumulate_strided_and_unaligned_outputs(cuda_lib, M, N, K, kind):
