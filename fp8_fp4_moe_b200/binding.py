@@ -190,34 +190,38 @@ def gemm_fp8_fp4(A, A_scales, B, B_scales, out=None, workspace=None, stream=None
     return out, workspace
 
 
+# the current stream's handle without a Stream object (a few times faster than torch.cuda.current_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(d, stream, call):
     """call(raw stream) with `stream` (default: d's current stream) and its device current, so that
     what the call allocates belongs to the stream that uses it."""
     if d.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, got {d}")
-    cur = torch.cuda.current_stream(d)
-    if (stream is None or stream == cur) and torch.cuda.current_device() == d.index:
-        return call(cur.cuda_stream)
+    if stream is None and torch.cuda.current_device() == d.index:
+        return call(_raw_stream(d.index))
     if stream is None:
-        stream = cur
+        stream = torch.cuda.current_stream(d)
     elif stream.device != d:
         raise ValueError(f"stream on {stream.device}, tensors on {d}")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
 
-def _matrix(name, t, shape, dtypes, device):
+def _matrix(name, t, rows, cols, dtypes, device):
     """Row pitch (elements) of a 2-D tensor whose rows are contiguous."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got shape {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(x) for x in dtypes]}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} on {t.device}, expected {device}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"the rows of {name} must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    return pitch if rows > 1 else max(cols, 1)
 
 
 def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, scale_dtype=torch.float32,
@@ -240,7 +244,7 @@ def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, 
         raise ValueError("nothing to write: rows or cols")
     M, K = x.shape
     d = x.device
-    ldx = _matrix("x", x, (M, K), _TYPES, d)
+    ldx = _matrix("x", x, M, K, _TYPES, d)
     mb, kb = -(-M // 128), -(-K // 128)
     s_shape, st_shape = ((M, kb), (K, mb)) if block == "row" else ((mb, kb), (kb, mb))
 
@@ -248,13 +252,13 @@ def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, 
         def codes(n, m, given):
             if given is None:
                 ld = -(-m // 16) * 16
-                t = torch.empty((n, ld), dtype=dtype, device=d)
+                t = torch.empty(n, ld, dtype=dtype, device=d)
                 return (t if ld == m else t[:, :m]), ld
-            return given, _matrix("out", given, (n, m), (dtype,), d)
+            return given, _matrix("out", given, n, m, (dtype,), d)
 
         def scales(shape, given):
             if given is None:
-                return torch.empty((shape[1], shape[0]), dtype=scale_dtype, device=d).t()
+                return torch.empty_strided(shape, (1, shape[0]), dtype=scale_dtype, device=d)
             if given.shape != shape or given.dtype != scale_dtype or given.device != d:
                 raise ValueError(f"out scales must be {list(shape)} of {scale_dtype} on {d}")
             return given
@@ -304,8 +308,8 @@ def gemm_fp8(A, A_scales, B, B_scales, out=None, out_dtype=torch.bfloat16, accum
     M, K = A.shape
     N = B.shape[0]
     d = A.device
-    lda = _matrix("A", A, (M, K), _FORMATS, d)
-    ldb = _matrix("B", B, (N, K), _FORMATS, d)
+    lda = _matrix("A", A, M, K, _FORMATS, d)
+    ldb = _matrix("B", B, N, K, _FORMATS, d)
     kb = -(-K // 128)
     if A_scales.dtype not in _SCALES:
         raise TypeError(f"scales must be float32 or uint8 (UE8M0), got {A_scales.dtype}")
@@ -314,12 +318,12 @@ def gemm_fp8(A, A_scales, B, B_scales, out=None, out_dtype=torch.bfloat16, accum
     if accumulate and out is None:
         raise ValueError("accumulate needs the out to add to")
     odt = out_dtype if out is None else out.dtype
-    if odt is not torch.bfloat16 and (odt is not torch.float32):
+    if odt is not torch.bfloat16 and odt is not torch.float32:
         raise TypeError(f"out must be bfloat16 or float32, got {odt}")
-    ldo = N if out is None else _matrix("out", out, (M, N), (odt,), d)
+    ldo = N if out is None else _matrix("out", out, M, N, (odt,), d)
 
     def call(sp):
-        o = torch.empty((M, N), dtype=odt, device=d) if out is None else out
+        o = torch.empty(M, N, dtype=odt, device=d) if out is None else out
         ws = torch.empty(256, dtype=torch.uint8, device=d) if workspace is None else workspace
         rc = lib().moe_gemm_fp8(M, N, K, A.data_ptr(), lda, _FORMATS[A.dtype], A_scales.data_ptr(),
                                 *A_scales.stride(), ar, B.data_ptr(), ldb, _FORMATS[B.dtype], B_scales.data_ptr(),
@@ -336,7 +340,7 @@ def _balance_args(logits, offsets, mask, score):
         raise ValueError(f"logits must be [T, E], got shape {tuple(logits.shape)}")
     T, E = logits.shape
     d = logits.device
-    ldl = _matrix("logits", logits, (T, E), (torch.float32, torch.bfloat16), d)
+    ldl = _matrix("logits", logits, T, E, (torch.float32, torch.bfloat16), d)
     if score not in _SCORES:
         raise ValueError(f"score must be one of {list(_SCORES)}, got {score!r}")
     S, op, mp = 1, None, None
@@ -368,8 +372,8 @@ def balance_loss(logits, topk_ids, coef=1.0, offsets=None, mask=None, score="sof
     def call(sp):
         ws = torch.empty(need, dtype=torch.uint8, device=d) if workspace is None else workspace
         loss = torch.empty((), dtype=torch.float32, device=d)
-        counts = torch.empty((S, E), dtype=torch.int32, device=d)
-        probs = torch.empty((S, E), dtype=torch.float32, device=d)
+        counts = torch.empty(S, E, dtype=torch.int32, device=d)
+        probs = torch.empty(S, E, dtype=torch.float32, device=d)
         tokens = torch.empty(S, dtype=torch.int32, device=d)
         rc = L.moe_balance_loss(T, E, k, S, logits.data_ptr(), ldl, _TYPES[logits.dtype], ids, op, mp, _SCORES[score],
                                 coef, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(),
@@ -392,10 +396,10 @@ def balance_loss_backward(grad_loss, logits, counts, tokens, k: int, coef=1.0, o
     gp, cp, np_ = _ptr(grad_loss, torch.float32, d), _ptr(counts, torch.int32, d), _ptr(tokens, torch.int32, d)
     if accumulate and out is None:
         raise ValueError("accumulate needs the out to add to")
-    ldg = E if out is None else _matrix("out", out, (T, E), (logits.dtype,), d)
+    ldg = E if out is None else _matrix("out", out, T, E, (logits.dtype,), d)
 
     def call(sp):
-        g = torch.empty((T, E), dtype=logits.dtype, device=d) if out is None else out
+        g = torch.empty(T, E, dtype=logits.dtype, device=d) if out is None else out
         rc = lib().moe_balance_loss_backward(T, E, k, S, gp, logits.data_ptr(), ldl, _TYPES[logits.dtype], cp, np_,
                                              op, mp, _SCORES[score], coef, g.data_ptr(), ldg, accumulate, sp)
         _check(rc, "moe_balance_loss_backward")

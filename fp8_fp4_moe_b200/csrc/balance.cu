@@ -24,7 +24,8 @@ namespace {
 constexpr int kWarps = 8;
 
 struct BalanceArgs {
-  int T, E, k, S, chunk, chunks;
+  int T, E, k, S, chunk, chunks, score;
+  int one_launch;            // the cluster kernel did everything
   const void* logits;
   long ldl;
   const int32_t* ids;        // [T, k]
@@ -35,6 +36,7 @@ struct BalanceArgs {
   float* part_p;             // [slots][E]
   int32_t* part_c;           // [slots][E]
   int32_t* part_n;           // [slots]
+  double* part_l;            // [S][ceil(E / 8)]: sums of counts * probs / n
   uint32_t* ticket;
   // results
   float* loss;
@@ -48,142 +50,234 @@ struct BalanceArgs {
   int accumulate;
 };
 
-// First token of sequence s (0..S), inside [0, T] whatever the array holds.
-__device__ __forceinline__ int seq_start(const BalanceArgs& p, int s) {
-  if (p.offsets == nullptr) return s == 0 ? 0 : p.T;
-  return min(max(p.offsets[s], 0), p.T);
-}
-// The largest s in [-1, S] with seq_start(s) <= t (offsets ascend): the sequence of token t, or -1 / S
-// for a token before the first or behind the last one.
-__device__ __forceinline__ int seq_of(const BalanceArgs& p, int t) {
-  if (p.offsets == nullptr) return 0;
-  int lo = -1, hi = p.S;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo + 1) / 2;
-    if (seq_start(p, mid) <= t) lo = mid; else hi = mid - 1;
+// First tokens of the sequences, inside [0, T] whatever the array holds.  Up to kStarts of them lie in shared
+// memory, where a search does not pay a trip to L2 a step.
+constexpr int kStarts = 1025;
+struct Starts {
+  const int32_t* at;                 // shared or global, NULL: one sequence of all tokens
+  int S, T;
+  __device__ __forceinline__ int operator[](int s) const {
+    if (at == nullptr) return s == 0 ? 0 : T;
+    return min(max(at[s], 0), T);
   }
-  return lo;
+  // The largest s in [-1, S] with start <= t (they ascend): the sequence of token t, or -1 / S for a token
+  // before the first or behind the last one.
+  __device__ __forceinline__ int of(int t) const {
+    if (at == nullptr) return 0;
+    int lo = -1, hi = S;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if ((*this)[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+// All threads call it; a barrier follows before the result is used.
+__device__ __forceinline__ Starts stage_starts(const BalanceArgs& p, int32_t* smem) {
+  if (p.offsets == nullptr || p.S + 1 > kStarts) return Starts{p.offsets, p.S, p.T};
+  for (int i = threadIdx.x; i <= p.S; i += blockDim.x) smem[i] = p.offsets[i];
+  return Starts{smem, p.S, p.T};
 }
 
-template <class T>
-__device__ __forceinline__ float load1(const T* p);
-template <>
-__device__ __forceinline__ float load1<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load1<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
-__device__ __forceinline__ float warp_sum(float v) {
+// How a token's E logits lie over lanes: LPR lanes to a row (32 / LPR rows to a warp), J logits to a lane; V
+// consecutive ones load together.  Eight lanes with 32 logits each make 256 of them: a sum or maximum over the
+// row is three shuffles for four rows, where a row to a warp takes five for each.
+template <class T, int LPR, int J, int V>
+struct RowMap {
+  static constexpr int kRows = 32 / LPR;
+  static __device__ __forceinline__ int expert(int lane, int j) {
+    return V == 1 ? lane % LPR + LPR * j : V * (lane % LPR) + j % V + V * LPR * (j / V);
+  }
+  static __device__ __forceinline__ void load(const T* row, int E, int lane, bool live, float (&l)[J]) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int j = 0; j < J; j += V) {
+      const int e = expert(lane, j);
+      if constexpr (V == 4 && sizeof(T) == 4) {
+        const float4 v = live && e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
+                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        l[j] = v.x;
+        l[j + 1] = v.y;
+        l[j + 2] = v.z;
+        l[j + 3] = v.w;
+      } else if constexpr (V == 4) {
+        const uint2 v = live && e < E ? __ldg(reinterpret_cast<const uint2*>(row + e)) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+        l[j] = __uint_as_float(v.x << 16);
+        l[j + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+        l[j + 2] = __uint_as_float(v.y << 16);
+        l[j + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+      } else if constexpr (sizeof(T) == 4) {
+        l[j] = live && e < E ? __ldg(row + e) : -INFINITY;
+      } else {
+        l[j] = live && e < E ? __bfloat162float(row[e]) : -INFINITY;
+      }
+    }
+  }
+};
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = LPR / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
-template <int J>
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// exp(l - m) as 2^(l log2(e) - m log2(e)), one FMA: the rounding of m log2(e) is common to the row and cancels in the
+// quotient, that of the result is at most that of l - m.
+template <int LPR, int J>
 __device__ __forceinline__ void softmax_row(float (&l)[J]) {
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < J; ++j) m = fmaxf(m, l[j]);
-  m = warp_max(m);
+  m = row_max<LPR>(m);
   float z = 0.f;
+  if (__any_sync(0xffffffffu, fabsf(m) > 1e30f)) {   // m log2(e) may overflow, or nothing is finite
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    l[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - m);
-    z += l[j];
+    for (int j = 0; j < J; ++j) {
+      l[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - m);
+      z += l[j];
+    }
+  } else {
+    const float ml = -m * kLog2e;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      l[j] = ex2(fmaf(l[j], kLog2e, ml));
+      z += l[j];
+    }
   }
-  z = warp_sum(z);
+  z = row_sum<LPR>(z);
   const float r = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
   for (int j = 0; j < J; ++j) l[j] *= r;
 }
 
-// Scores of one token: lane holds experts lane + 32 j.  sg = sigma(l) (sigmoid scores).  A row whose
-// logits are all -inf has zero scores.
-template <int J, bool SIG>
-__device__ __forceinline__ void scores(float (&l)[J], float (&sg)[J]) {
-  if constexpr (SIG) {
-    float z = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      sg[j] = 1.f / (1.f + expf(-l[j]));
-      z += sg[j];
-    }
-    z = warp_sum(z);
-    if (z < 1e-30f) {                  // every sigma underflows: the same scores from their logarithms
-#pragma unroll
-      for (int j = 0; j < J; ++j) l[j] = fminf(l[j], 0.f) - log1pf(expf(-fabsf(l[j])));
-      softmax_row<J>(l);
-      return;
-    }
-    const float r = 1.f / z;
-#pragma unroll
-    for (int j = 0; j < J; ++j) l[j] = sg[j] * r;
-  } else {
-    softmax_row<J>(l);
+// l: a token's logits -> its scores; returns Z = sum of sigma(l) for sigmoid scores, so that sigma = l Z (0: they are
+// too small for that, and 1 - sigma is 1).  A row whose logits are all -inf has zero scores, and so has a token
+// that does not count (not live: its logits read as -inf).  All lanes of the warp call it.
+template <int LPR, int J>
+__device__ __forceinline__ float scores(int score, bool live, float (&l)[J]) {
+  if (score != MOE_SCORE_SIGMOID) {
+    softmax_row<LPR, J>(l);
+    return 0.f;
   }
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) z += __fdividef(1.f, 1.f + ex2(-l[j] * kLog2e));
+  z = row_sum<LPR>(z);
+  const bool tiny = live && z < 1e-30f;
+  if (__any_sync(0xffffffffu, tiny)) { // every sigma of a row underflows: the warp's rows from their logarithms
+#pragma unroll
+    for (int j = 0; j < J; ++j) l[j] = fminf(l[j], 0.f) - log1pf(expf(-fabsf(l[j])));
+    softmax_row<LPR, J>(l);
+  } else {
+    const float r = live ? 1.f / z : 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) l[j] = __fdividef(1.f, 1.f + ex2(-l[j] * kLog2e)) * r;
+  }
+  return tiny ? 0.f : z;
 }
 
-template <class T, int J>
-__device__ __forceinline__ void load_row(const BalanceArgs& p, int t, int lane, float (&l)[J]) {
-  const T* row = static_cast<const T*>(p.logits) + (long)t * p.ldl;
+// Sums over tokens [a, b) by one block: sum_s[warp][E] of scores, cnt_s[E] of choices, n_s tokens that count.  The
+// next round's rows are on their way while one is computed.  A barrier stands at the end.
+template <class T, int LPR, int J, int V, int U>
+__device__ __forceinline__ void sum_tokens(const BalanceArgs& p, int a, int b, float* sum_s, int* cnt_s, int& n_s) {
+  using Map = RowMap<T, LPR, J, V>;
+  constexpr int kStep = kWarps * Map::kRows;                // tokens of the block a round of one row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < p.E; e += kWarps * 32) cnt_s[e] = 0;
+  if (threadIdx.x == 0) n_s = 0;
+  float acc[J], l[U][J];
+  bool live[U];
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[j] = 0.f;
+  auto load = [&](int r0, float (&x)[U][J], bool (&on)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = r0 + u * kStep + lane / LPR;
+      on[u] = t < b && (p.mask == nullptr || p.mask[t] != 0);
+      Map::load(static_cast<const T*>(p.logits) + (long)t * p.ldl, p.E, lane, on[u], x[u]);
+    }
+  };
+  int r0 = a + warp * Map::kRows;
+  if (r0 < b) load(r0, l, live);
+  // choices of these tokens
+  __syncthreads();
+  const int32_t* ids = p.ids + (long)a * p.k;
+  for (int i = threadIdx.x; i < (b - a) * p.k; i += kWarps * 32) {
+    const int e = ids[i];
+    if ((unsigned)e < (unsigned)p.E && (p.mask == nullptr || p.mask[a + i / p.k] != 0)) atomicAdd(&cnt_s[e], 1);
+  }
+  for (; r0 < b; r0 += U * kStep) {
+    float next[U][J];
+    bool on[U];
+    load(r0 + U * kStep, next, on);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      n += live[u] && lane % LPR == 0;
+      if (u == 0 || __any_sync(0xffffffffu, live[u])) {
+        scores<LPR, J>(p.score, live[u], l[u]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[j] += l[u][j];
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) l[u][j] = next[u][j];
+      live[u] = on[u];
+    }
+  }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane + 32 * j;
-    l[j] = e < p.E ? load1<T>(row + e) : -INFINITY;
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    const int e = Map::expert(lane, j);
+    if (lane < LPR && e < p.E) sum_s[warp * p.E + e] = acc[j];
   }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n > 0) atomicAdd(&n_s, n);
+  __syncthreads();
+}
+
+__device__ __forceinline__ float warps_sum(const BalanceArgs& p, const float* sum_s, int e) {
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += sum_s[w * p.E + e];
+  return v;
 }
 
 // Partial sums of one chunk of tokens, a slot per sequence that the chunk touches: (chunk, sequence)
-// pairs ascend in both, so chunk + sequence numbers them without gaps being shared.
-template <class T, int J, bool SIG>
-__global__ void __launch_bounds__(kWarps * 32) balance_part_kernel(const BalanceArgs p) {
+// pairs ascend in both, so chunk + sequence numbers them without two sharing a number.
+template <class T, int LPR, int J, int V, int U>
+__global__ void __launch_bounds__(kWarps * 32, 2) balance_part_kernel(const BalanceArgs p) {
   extern __shared__ float sm[];
   float* sum_s = sm;                                        // [kWarps][E]
   int* cnt_s = reinterpret_cast<int*>(sm + kWarps * p.E);   // [E]
   __shared__ int n_s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int32_t starts_s[kStarts];
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
+  const Starts start = stage_starts(p, starts_s);
+  __syncthreads();
+  griddep_launch_dependents();         // the join kernel's blocks may wait on the device already
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
-  int s = max(0, seq_of(p, t0));
-  for (; s < p.S; ++s) {
-    const int a = max(t0, seq_start(p, s)), b = min(t1, seq_start(p, s + 1));
-    if (seq_start(p, s) >= t1) break;
+  for (int s = max(0, start.of(t0)); s < p.S; ++s) {
+    const int a = max(t0, start[s]), b = min(t1, start[s + 1]);
+    if (start[s] >= t1) break;
     if (a >= b) continue;
-    for (int e = threadIdx.x; e < p.E; e += kWarps * 32) cnt_s[e] = 0;
-    if (threadIdx.x == 0) n_s = 0;
-    __syncthreads();
-    float acc[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) acc[j] = 0.f;
-    int n = 0;
-    for (int t = a + warp; t < b; t += kWarps) {
-      if (p.mask != nullptr && p.mask[t] == 0) continue;
-      ++n;
-      float l[J], sg[J];
-      load_row<T, J>(p, t, lane, l);
-      for (int i = lane; i < p.k; i += 32) {
-        const int e = p.ids[(long)t * p.k + i];
-        if ((unsigned)e < (unsigned)p.E) atomicAdd(&cnt_s[e], 1);
-      }
-      scores<J, SIG>(l, sg);
-#pragma unroll
-      for (int j = 0; j < J; ++j) acc[j] += l[j];
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (lane + 32 * j < p.E) sum_s[warp * p.E + lane + 32 * j] = acc[j];
-    if (lane == 0) atomicAdd(&n_s, n);
-    __syncthreads();
+    sum_tokens<T, LPR, J, V, U>(p, a, b, sum_s, cnt_s, n_s);
     const long slot = blockIdx.x + s;
     for (int e = threadIdx.x; e < p.E; e += kWarps * 32) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += sum_s[w * p.E + e];
-      p.part_p[slot * p.E + e] = v;
+      p.part_p[slot * p.E + e] = warps_sum(p, sum_s, e);
       p.part_c[slot * p.E + e] = cnt_s[e];
     }
     if (threadIdx.x == 0) p.part_n[slot] = n_s;
@@ -191,78 +285,148 @@ __global__ void __launch_bounds__(kWarps * 32) balance_part_kernel(const Balance
   }
 }
 
-// One block per (sequence, 32 experts): the slots of the sequence added up in order.  The last block of
-// the grid adds up the loss.
-__global__ void __launch_bounds__(1024) balance_join_kernel(const BalanceArgs p) {
-  __shared__ float fp[32][33];
-  __shared__ int fc[32][33];
-  __shared__ int fn[32];
+// One sequence of few tokens: the blocks of one cluster have a share of the tokens each, then of the experts, whose
+// sums they add up in rank order through distributed shared memory.  One launch instead of two.
+constexpr int kCluster = 8;
+constexpr int kClusterRounds = 8;      // rounds of rows a block of the cluster takes at most
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+template <class T, int LPR, int J, int V, int U>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWarps * 32, 2)
+    balance_cluster_kernel(const BalanceArgs p) {
+  extern __shared__ float sm[];
+  float* sum_s = sm;
+  int* cnt_s = reinterpret_cast<int*>(sm + kWarps * p.E);
+  __shared__ int n_s;
+  __shared__ double part_s[kCluster];
+  __shared__ double warp_s[kWarps];
+  const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int a = min(p.T, rank * p.chunk), b = min(p.T, a + p.chunk);
+  sum_tokens<T, LPR, J, V, U>(p, a, b, sum_s, cnt_s, n_s);
+  for (int e = threadIdx.x; e < p.E; e += kWarps * 32) sum_s[e] = warps_sum(p, sum_s, e);   // column e is this thread's
+  __syncthreads();
+  cluster_sync();
+  int n = 0;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) n += (int)ld_cluster(mapa_shared(&n_s, r));
+  const float inv = n > 0 ? (float)n : 1.f;
+  double v = 0.0;
+  for (int e = rank + kCluster * threadIdx.x; e < p.E; e += kCluster * kWarps * 32) {
+    float sum = 0.f;
+    int c = 0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) {
+      sum += __uint_as_float(ld_cluster(mapa_shared(sum_s + e, r)));
+      c += (int)ld_cluster(mapa_shared(cnt_s + e, r));
+    }
+    const float mean = n > 0 ? sum / inv : 0.f;
+    p.counts[e] = c;
+    p.probs[e] = mean;
+    v += (double)c * (double)mean;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) warp_s[warp] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += warp_s[w];
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(part_s + rank, 0)), "d"(v) : "memory");
+  }
+  __syncthreads();
+  cluster_sync();                      // no block leaves while another reads its sums
+  if (rank == 0 && threadIdx.x == 0) {
+    v = 0.0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) v += part_s[r];
+    p.tokens[0] = n;
+    *p.loss = n > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)n)) : 0.f;
+  }
+}
+
+// One block per (sequence, 8 experts): the slots of the sequence added up in order, every 32nd by one thread.
+// The last block of the grid adds up the loss.
+constexpr int kJoin = 32;
+__global__ void __launch_bounds__(kJoin * 8) balance_join_kernel(const BalanceArgs p) {
+  __shared__ float fp[kJoin][8];
+  __shared__ int fc[kJoin][8];
+  __shared__ int fn[kJoin];
   __shared__ bool last;
   griddep_wait();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int s = blockIdx.x, e = blockIdx.y * 32 + lane;
-  const int a = seq_start(p, s), b = seq_start(p, s + 1);
+  const int x = threadIdx.x & 7, w = threadIdx.x >> 3;
+  const int s = blockIdx.x, e = blockIdx.y * 8 + x;
+  const Starts start{p.offsets, p.S, p.T};
+  const int a = start[s], b = start[s + 1];
   const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk + 1 : c0;   // chunks of the sequence
   float vp = 0.f;
   int vc = 0, vn = 0;
-  for (int c = c0 + w; c < c1; c += 32) {
+#pragma unroll 8
+  for (int c = c0 + w; c < c1; c += kJoin) {
     const long slot = c + s;
     if (e < p.E) {
       vp += p.part_p[slot * p.E + e];
       vc += p.part_c[slot * p.E + e];
     }
-    if (lane == 0) vn += p.part_n[slot];
+    vn += p.part_n[slot];
   }
-  fp[w][lane] = vp;
-  fc[w][lane] = vc;
-  if (lane == 0) fn[w] = vn;
+  fp[w][x] = vp;
+  fc[w][x] = vc;
+  if (x == 0) fn[w] = vn;
   __syncthreads();
-  if (w == 0) {
+  if (threadIdx.x < 32) {              // lanes 8 and up repeat the first ones' experts
     vp = 0.f;
     vc = vn = 0;
-    for (int i = 0; i < 32; ++i) {
-      vp += fp[i][lane];
-      vc += fc[i][lane];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      vp += fp[i][x];
+      vc += fc[i][x];
       vn += fn[i];
     }
-    if (e < p.E) {
+    const float mean = vn > 0 ? vp / (float)vn : 0.f;
+    if (w == 0 && e < p.E) {
       p.counts[(long)s * p.E + e] = vc;
-      p.probs[(long)s * p.E + e] = vn > 0 ? vp / (float)vn : 0.f;
+      p.probs[(long)s * p.E + e] = mean;
     }
-    if (blockIdx.y == 0 && lane == 0) p.tokens[s] = vn;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
-    __threadfence();
+    double r = e < p.E && vn > 0 ? (double)vc * (double)mean / (double)vn : 0.0;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (threadIdx.x == 0) {
+      p.part_l[(long)s * gridDim.y + blockIdx.y] = r;
+      if (blockIdx.y == 0) p.tokens[s] = vn;
+      __threadfence();
+      last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
+      __threadfence();
+    }
   }
   __syncthreads();
   if (!last) return;
-  // 64-bit sums: S * E terms of one sign each
+  // the loss, in 64 bits: terms of one sign, in a fixed order
   double v = 0.0;
   int live = 0;
-  for (int q = w; q < p.S; q += 32) {
-    const int n = __ldcg(p.tokens + q);
-    if (n <= 0) continue;
-    live += lane == 0;
-    double r = 0.0;
-    for (int i = lane; i < p.E; i += 32)
-      r += (double)__ldcg(p.counts + (long)q * p.E + i) * (double)__ldcg(p.probs + (long)q * p.E + i);
-    v += r / (double)n;
-  }
+  const int terms = gridDim.x * gridDim.y;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < terms; i += kJoin * 8) v += __ldcg(p.part_l + i);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.S; i += kJoin * 8) live += __ldcg(p.tokens + i) > 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __shared__ double lv[32];
+  live = __reduce_add_sync(0xffffffffu, live);
+  __shared__ double lv[kJoin / 4];
   if (lane == 0) {
-    lv[w] = v;
-    fn[w] = live;
+    lv[warp] = v;
+    fn[warp] = live;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     v = 0.0;
     live = 0;
-    for (int i = 0; i < 32; ++i) {
+#pragma unroll
+    for (int i = 0; i < kJoin / 4; ++i) {
       v += lv[i];
       live += fn[i];
     }
@@ -270,57 +434,112 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(const BalanceArgs p)
   }
 }
 
-template <class T>
-__device__ __forceinline__ void put(T* p, float v, int accumulate);
-template <>
-__device__ __forceinline__ void put<float>(float* p, float v, int accumulate) { *p = accumulate ? *p + v : v; }
-template <>
-__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* p, float v, int accumulate) {
-  *p = __float2bfloat16_rn(accumulate ? __bfloat162float(*p) + v : v);
-}
-
-// A warp per token.  Tokens outside every sequence and masked tokens get zeros (or stay, accumulating).
-template <class T, int J, bool SIG>
-__global__ void __launch_bounds__(kWarps * 32) balance_grad_kernel(const BalanceArgs p) {
+// Tokens outside every sequence and masked tokens get zeros (or stay, accumulating).
+template <class T, int LPR, int J, int V, int U>
+__global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const BalanceArgs p) {
+  using Map = RowMap<T, LPR, J, V>;
   __shared__ int live_s;
+  __shared__ int32_t starts_s[kStarts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) live_s = 0;
+  const Starts start = stage_starts(p, starts_s);
   __syncthreads();
-  int live = 0;
-  for (int s = threadIdx.x; s < p.S; s += kWarps * 32) live += p.tokens[s] > 0;
-  if (live) atomicAdd(&live_s, live);
+  int alive = 0;
+  for (int s = threadIdx.x; s < p.S; s += kWarps * 32) alive += p.tokens[s] > 0;
+  if (alive) atomicAdd(&live_s, alive);
   __syncthreads();
   const float base = *p.grad_loss * p.coef * (float)p.E / ((float)p.k * (float)max(1, live_s));
-  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
-    const int s = seq_of(p, t);
-    T* out = static_cast<T*>(p.grad) + (long)t * p.ldg;
-    if (s < 0 || s >= p.S || t >= seq_start(p, s + 1) || (p.mask != nullptr && p.mask[t] == 0) || p.tokens[s] <= 0) {
-      if (!p.accumulate) {
+  const int step = gridDim.x * kWarps * Map::kRows;
+  int have = -1;                       // the sequence that c and g are of
+  float c[J], g = 0.f;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (lane + 32 * j < p.E) put<T>(out + lane + 32 * j, 0.f, 0);
+  for (int j = 0; j < J; ++j) c[j] = 0.f;
+  float l[U][J];
+  int seq[U];                          // -1: the token does not count
+  auto load = [&](int r0, float (&x)[U][J], int (&of)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = r0 + u * step + lane / LPR;
+      of[u] = -1;
+      if (t < p.T && (p.mask == nullptr || p.mask[t] != 0)) {
+        const int s = start.of(t);
+        if (s >= 0 && s < p.S && t < start[s + 1]) of[u] = s;
       }
-      continue;
+      Map::load(static_cast<const T*>(p.logits) + (long)t * p.ldl, p.E, lane, of[u] >= 0, x[u]);
     }
-    float l[J], sg[J], c[J];
-    load_row<T, J>(p, t, lane, l);
+  };
+  int r0 = (blockIdx.x * kWarps + warp) * Map::kRows;
+  if (r0 < p.T) load(r0, l, seq);
+  for (; r0 < p.T; r0 += U * step) {
+    float next[U][J];                  // on their way while these are computed
+    int of[U];
+    load(r0 + U * step, next, of);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int e = lane + 32 * j;
-      c[j] = e < p.E ? (float)__ldg(p.counts + (long)s * p.E + e) : 0.f;
+    for (int u = 0; u < U; ++u) {
+      const int t = r0 + u * step + lane / LPR;
+      if (u > 0 && r0 + u * step >= p.T) break;            // the whole warp
+      if (seq[u] >= 0 && seq[u] != have) {
+        have = seq[u];
+        const int32_t* cs = p.counts + (long)have * p.E;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int e = Map::expert(lane, j);
+          c[j] = e < p.E ? (float)__ldg(cs + e) : 0.f;
+        }
+        const float n = (float)max(1, p.tokens[have]);
+        g = base / n / n;
+      }
+      const float z = scores<LPR, J>(p.score, seq[u] >= 0, l[u]);
+      float mean = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) mean = fmaf(c[j], l[u][j], mean);
+      mean = row_sum<LPR>(mean);
+      const bool write = t < p.T && (seq[u] >= 0 || !p.accumulate);
+      T* out = static_cast<T*>(p.grad) + (long)t * p.ldg;
+#pragma unroll
+      for (int j = 0; j < J; j += V) {
+        float d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          d[v] = g * l[u][j + v] * (c[j + v] - mean);
+          if (p.score == MOE_SCORE_SIGMOID) d[v] *= 1.f - l[u][j + v] * z;
+          if (seq[u] < 0) d[v] = 0.f;
+        }
+        const int e = Map::expert(lane, j);
+        if (e >= p.E || !write) continue;
+        if constexpr (V == 4) {
+          if constexpr (sizeof(T) == 4) {
+            float4* o = reinterpret_cast<float4*>(out + e);
+            if (p.accumulate) {
+              const float4 x = *o;
+              *o = make_float4(x.x + d[0], x.y + d[1], x.z + d[2], x.w + d[3]);
+            } else {
+              *o = make_float4(d[0], d[1], d[2], d[3]);
+            }
+          } else {
+            uint2* o = reinterpret_cast<uint2*>(out + e);
+            if (p.accumulate) {
+              const uint2 x = *o;
+              d[0] += __uint_as_float(x.x << 16);
+              d[1] += __uint_as_float(x.x & 0xFFFF0000u);
+              d[2] += __uint_as_float(x.y << 16);
+              d[3] += __uint_as_float(x.y & 0xFFFF0000u);
+            }
+            __nv_bfloat162 h[2] = {__floats2bfloat162_rn(d[0], d[1]), __floats2bfloat162_rn(d[2], d[3])};
+            *o = *reinterpret_cast<const uint2*>(h);
+          }
+        } else if constexpr (sizeof(T) == 4) {
+          out[e] = p.accumulate ? out[e] + d[0] : d[0];
+        } else {
+          out[e] = __float2bfloat16_rn(p.accumulate ? __bfloat162float(out[e]) + d[0] : d[0]);
+        }
+      }
     }
-    scores<J, SIG>(l, sg);
-    float mean = 0.f;
 #pragma unroll
-    for (int j = 0; j < J; ++j) mean += c[j] * l[j];
-    mean = warp_sum(mean);
-    const float n = (float)p.tokens[s];
-    const float g = base / n / n;
+    for (int u = 0; u < U; ++u) {
+      seq[u] = of[u];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float d = g * l[j] * (c[j] - mean);
-      if constexpr (SIG) d *= 1.f - sg[j];
-      if (lane + 32 * j < p.E) put<T>(out + lane + 32 * j, d, p.accumulate);
+      for (int j = 0; j < J; ++j) l[u][j] = next[u][j];
     }
   }
 }
@@ -330,21 +549,22 @@ size_t r256(size_t b) { return (b + 255) & ~size_t(255); }
 
 struct Layout {
   int chunk, chunks;
-  size_t part_p, part_c, part_n, ticket, total;
+  size_t part_p, part_c, part_n, part_l, ticket, total;
 };
 
-// About two blocks per SM, and chunks of a multiple of the warps.
+// About two blocks per SM (with four rows of 1 KB to a warp, 64 KB of logits in flight an SM), and a round of
+// all warps at least.
 Layout layout(int T, int E, int S) {
   Layout L;
-  int chunk = (T + 2 * 148 - 1) / (2 * 148);
-  chunk = (chunk + kWarps - 1) / kWarps * kWarps;
-  L.chunk = chunk < kWarps ? kWarps : chunk;
+  const int chunk = ((T + 2 * 148 - 1) / (2 * 148) + 15) / 16 * 16;
+  L.chunk = chunk < 32 ? 32 : chunk;
   L.chunks = (T + L.chunk - 1) / L.chunk;
   const size_t slots = (size_t)L.chunks + (size_t)S;
   L.part_p = 0;
   L.part_c = L.part_p + r256(slots * E * 4);
   L.part_n = L.part_c + r256(slots * E * 4);
-  L.ticket = L.part_n + r256(slots * 4);
+  L.part_l = L.part_n + r256(slots * 4);
+  L.ticket = L.part_l + r256((size_t)S * ((E + 7) / 8) * 8);
   L.total = L.ticket + 256;
   return L;
 }
@@ -354,26 +574,37 @@ bool shape_ok(int T, int E, int k, int S) {
 }
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <class T, int J>
-cudaError_t launch_part(const BalanceArgs& a, int score, cudaStream_t s) {
+template <class T, int LPR, int J, int V, int U>
+cudaError_t launch_as(BalanceArgs& a, bool grad, cudaStream_t s) {
+  const int round = kWarps * 32 / LPR * U;                  // tokens of a block a round
+  if (grad) {
+    const int need = (a.T + kWarps * 32 / LPR - 1) / (kWarps * 32 / LPR);
+    balance_grad_kernel<T, LPR, J, V, U><<<need < 2 * 148 ? need : 2 * 148, kWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4;
-  auto f = score == MOE_SCORE_SIGMOID ? balance_part_kernel<T, J, true> : balance_part_kernel<T, J, false>;
-  f<<<a.chunks, kWarps * 32, smem, s>>>(a);
+  a.one_launch = a.offsets == nullptr && a.T <= kCluster * round * kClusterRounds;
+  if (a.one_launch) {
+    a.chunk = (a.T + kCluster - 1) / kCluster;
+    balance_cluster_kernel<T, LPR, J, V, U><<<kCluster, kWarps * 32, smem, s>>>(a);
+  } else {
+    balance_part_kernel<T, LPR, J, V, U><<<a.chunks, kWarps * 32, smem, s>>>(a);
+  }
   return cudaGetLastError();
 }
-template <class T, int J>
-cudaError_t launch_grad(const BalanceArgs& a, int score, cudaStream_t s) {
-  const int need = (a.T + kWarps - 1) / kWarps, grid = need < 148 * 8 ? need : 148 * 8;
-  auto f = score == MOE_SCORE_SIGMOID ? balance_grad_kernel<T, J, true> : balance_grad_kernel<T, J, false>;
-  f<<<grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
-}
+// vec: rows and pitches of whole groups of four logits
 template <class T>
-cudaError_t launch_any(const BalanceArgs& a, int score, bool grad, cudaStream_t s) {
-  const int j = (a.E + 31) / 32;
-#define MOE_J(N) (grad ? launch_grad<T, N>(a, score, s) : launch_part<T, N>(a, score, s))
-  return j <= 1 ? MOE_J(1) : j <= 2 ? MOE_J(2) : j <= 4 ? MOE_J(4) : j <= 8 ? MOE_J(8) : j <= 16 ? MOE_J(16) : MOE_J(32);
-#undef MOE_J
+cudaError_t launch_any(BalanceArgs& a, bool vec, bool grad, cudaStream_t s) {
+  if (a.E <= 8) return launch_as<T, 8, 1, 1, 4>(a, grad, s);
+  if (a.E <= 32) return vec ? launch_as<T, 8, 4, 4, 4>(a, grad, s) : launch_as<T, 8, 4, 1, 4>(a, grad, s);
+  if (a.E <= 64) return vec ? launch_as<T, 8, 8, 4, 2>(a, grad, s) : launch_as<T, 8, 8, 1, 2>(a, grad, s);
+  if (a.E <= 128) return vec ? launch_as<T, 8, 16, 4, 2>(a, grad, s) : launch_as<T, 8, 16, 1, 2>(a, grad, s);
+  if (a.E <= 256) return vec ? launch_as<T, 8, 32, 4, 1>(a, grad, s) : launch_as<T, 8, 32, 1, 1>(a, grad, s);
+  if (a.E <= 512) return vec ? launch_as<T, 16, 32, 4, 1>(a, grad, s) : launch_as<T, 16, 32, 1, 1>(a, grad, s);
+  return vec ? launch_as<T, 32, 32, 4, 1>(a, grad, s) : launch_as<T, 32, 32, 1, 1>(a, grad, s);
+}
+bool rows_of_four(const void* p, long long ld, int rows, int E, size_t size) {
+  return E % 4 == 0 && aligned(p, 4 * size) && (rows <= 1 || ld % 4 == 0);
 }
 
 }  // namespace
@@ -420,19 +651,32 @@ int moe_balance_loss(int T, int E, int k, int S, const void* logits, long long l
   a.offsets = offsets;
   a.mask = mask;
   a.coef = coef;
+  a.score = score;
   a.part_p = reinterpret_cast<float*>(ws + L.part_p);
   a.part_c = reinterpret_cast<int32_t*>(ws + L.part_c);
   a.part_n = reinterpret_cast<int32_t*>(ws + L.part_n);
+  a.part_l = reinterpret_cast<double*>(ws + L.part_l);
   a.ticket = reinterpret_cast<uint32_t*>(ws + L.ticket);
   a.loss = loss;
   a.counts = counts;
   a.probs = probs;
   a.tokens = tokens;
-  cudaError_t e = logits_type == MOE_TYPE_FP32 ? launch_any<float>(a, score, false, s)
-                                               : launch_any<__nv_bfloat16>(a, score, false, s);
+  const bool vec = rows_of_four(logits, ldl, T, E, logits_type == MOE_TYPE_FP32 ? 4 : 2);
+  cudaError_t e = logits_type == MOE_TYPE_FP32 ? launch_any<float>(a, vec, false, s)
+                                               : launch_any<__nv_bfloat16>(a, vec, false, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  balance_join_kernel<<<dim3(S, (E + 31) / 32), 1024, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  if (a.one_launch) return MOE_OK;
+  // a programmatic dependent: its blocks are placed while the first kernel ends (griddep_wait)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(S, (E + 7) / 8);
+  cfg.blockDim = dim3(kJoin * 8);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int moe_balance_loss_backward(int T, int E, int k, int S, const float* grad_loss, const void* logits, long long ldl,
@@ -458,6 +702,7 @@ int moe_balance_loss_backward(int T, int E, int k, int S, const float* grad_loss
   a.offsets = offsets;
   a.mask = mask;
   a.coef = coef;
+  a.score = score;
   a.counts = const_cast<int32_t*>(counts);
   a.tokens = const_cast<int32_t*>(tokens);
   a.grad_loss = grad_loss;
@@ -465,8 +710,9 @@ int moe_balance_loss_backward(int T, int E, int k, int S, const float* grad_loss
   a.ldg = ldg;
   a.accumulate = accumulate != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = logits_type == MOE_TYPE_FP32 ? launch_any<float>(a, score, true, s)
-                                               : launch_any<__nv_bfloat16>(a, score, true, s);
+  const bool vec = rows_of_four(logits, ldl, T, E, es) && rows_of_four(grad_logits, ldg, T, E, es);
+  cudaError_t e = logits_type == MOE_TYPE_FP32 ? launch_any<float>(a, vec, true, s)
+                                               : launch_any<__nv_bfloat16>(a, vec, true, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
