@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libmoe_b200.so (argument marshalling only).
+"""Thin binding of libmoe_b200.so (argument marshalling only): ctypes, and for the operators that decode
+and training call many times a step the native _moe_ops.
 
 PyTorch provides device memory and streams; every step of the layer runs in
 the library's CUDA kernels.  There is no fallback: if the library is missing
@@ -38,13 +39,6 @@ MOE_OPT_L2_TILE_ROWS = 12
 MOE_OPT_CHAIN = 13
 MOE_OPT_TILE_ROWS = 14
 MOE_OPT_ZERO_PAD = 15
-
-# FP8 products and the balance loss (moe_type, moe_fp8_format, moe_scale_type, moe_block, moe_score)
-_TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
-_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.uint8: 0}   # plain bytes are E4M3 codes
-_SCALES = {torch.float32: 0, torch.uint8: 1}
-_BLOCKS = {"row": 0, "tile": 1}
-_SCORES = {"softmax": 0, "sigmoid": 1}
 
 PHASES = ["router", "topk_rank", "scan", "scatter_quant", "prepare", "linear1", "linear2", "combine"]
 
@@ -190,38 +184,45 @@ def gemm_fp8_fp4(A, A_scales, B, B_scales, out=None, workspace=None, stream=None
     return out, workspace
 
 
-# the current stream's handle without a Stream object (a few times faster than torch.cuda.current_stream)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_native = None
 
 
-def _run(d, stream, call):
-    """call(raw stream) with `stream` (default: d's current stream) and its device current, so that
-    what the call allocates belongs to the stream that uses it."""
-    if d.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {d}")
-    if stream is None and torch.cuda.current_device() == d.index:
-        return call(_raw_stream(d.index))
+def _ops():
+    """The native part of the binding (csrc/ops_binding.cpp): argument checks, output allocation and the
+    C-ABI calls of the functions below, on the tensors' device and its current stream."""
+    global _native
+    if _native is None:
+        lib()
+        path = os.path.join(_DIR, "_moe_ops.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing; build it with `python -m fp8_fp4_moe_b200.build`")
+        from . import _moe_ops
+        _native = _moe_ops
+    return _native
+
+
+def _call(name, stream, tensor, *args):
+    """A native function on `stream` (default: the current stream of the tensors' device), with it and its
+    device current, so that what the call allocates belongs to the stream that uses it."""
+    f = getattr(_native or _ops(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(d)
-    elif stream.device != d:
-        raise ValueError(f"stream on {stream.device}, tensors on {d}")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        r = f(*args)
+    else:
+        if tensor.is_cuda and stream.device != tensor.device:
+            raise ValueError(f"stream on {stream.device}, tensors on {tensor.device}")
+        with torch.cuda.stream(stream):
+            r = f(*args)
+    if type(r) is int:
+        raise MoeError(r, "moe_" + name)
+    return r
 
 
-def _matrix(name, t, rows, cols, dtypes, device):
-    """Row pitch (elements) of a 2-D tensor whose rows are contiguous."""
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got shape {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {[str(x) for x in dtypes]}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} on {t.device}, expected {device}")
-    pitch, step = t.stride()
-    if cols > 1 and step != 1:
-        raise ValueError(f"the rows of {name} must be contiguous, got strides {t.stride()}")
-    return pitch if rows > 1 else max(cols, 1)
+def _choice(name, value, one, other):
+    if value == one:
+        return False
+    if value == other:
+        return True
+    raise ValueError(f"{name} must be {one!r} or {other!r}, got {value!r}")
 
 
 def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, scale_dtype=torch.float32,
@@ -234,66 +235,9 @@ def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, 
     blocked along M, and st [K or ceil(K/128), ceil(M/128)]; None for what is not asked for.  Scales are
     fp32 or (scale_dtype torch.uint8) UE8M0 codes, stored so that those of consecutive rows are adjacent,
     and row pitches of the codes are multiples of 16: what gemm_fp8 takes.  `out`: the four to write."""
-    if x.dim() != 2:
-        raise ValueError(f"x must be [M, K], got shape {tuple(x.shape)}")
-    if block not in _BLOCKS:
-        raise ValueError(f"block must be one of {list(_BLOCKS)}, got {block!r}")
-    if dtype not in _FORMATS or scale_dtype not in _SCALES:
-        raise TypeError(f"no codes of {dtype} with scales of {scale_dtype}")
-    if not rows and not cols:
-        raise ValueError("nothing to write: rows or cols")
-    M, K = x.shape
-    d = x.device
-    ldx = _matrix("x", x, M, K, _TYPES, d)
-    mb, kb = -(-M // 128), -(-K // 128)
-    s_shape, st_shape = ((M, kb), (K, mb)) if block == "row" else ((mb, kb), (kb, mb))
-
-    def call(sp):
-        def codes(n, m, given):
-            if given is None:
-                ld = -(-m // 16) * 16
-                t = torch.empty(n, ld, dtype=dtype, device=d)
-                return (t if ld == m else t[:, :m]), ld
-            return given, _matrix("out", given, n, m, (dtype,), d)
-
-        def scales(shape, given):
-            if given is None:
-                return torch.empty_strided(shape, (1, shape[0]), dtype=scale_dtype, device=d)
-            if given.shape != shape or given.dtype != scale_dtype or given.device != d:
-                raise ValueError(f"out scales must be {list(shape)} of {scale_dtype} on {d}")
-            return given
-
-        q, s, qt, st = out if out is not None else (None, None, None, None)
-        a, b = [None, 0, None, 0, 0], [None, 0, None, 0, 0]
-        if rows:
-            q, ld = codes(M, K, q)
-            s = scales(s_shape, s)
-            a = [q.data_ptr(), ld, s.data_ptr(), *s.stride()]
-        else:
-            q = s = None
-        if cols:
-            qt, ld = codes(K, M, qt)
-            st = scales(st_shape, st)
-            b = [qt.data_ptr(), ld, st.data_ptr(), *st.stride()]
-        else:
-            qt = st = None
-        rc = lib().moe_quant_fp8(M, K, x.data_ptr(), ldx, _TYPES[x.dtype], _BLOCKS[block], _FORMATS[dtype],
-                                 _SCALES[scale_dtype], *a, *b, sp)
-        _check(rc, "moe_quant_fp8")
-        return q, s, qt, st
-
-    return _run(d, stream, call)
-
-
-def _scale_rows(name, s, rows, kb, dtype, device):
-    """1 for a scale per row, 128 for one per 128 rows."""
-    if s.dtype != dtype or s.device != device:
-        raise TypeError(f"{name} must be {dtype} on {device}, got {s.dtype} on {s.device}")
-    if s.shape == (rows, kb):
-        return 1
-    if s.shape == (-(-rows // 128), kb):
-        return 128
-    raise ValueError(f"{name} must be [{rows}, {kb}] or [{-(-rows // 128)}, {kb}], got shape {tuple(s.shape)}")
+    q, s, qt, st = (None, None, None, None) if out is None else out
+    return _call("quant_fp8", stream, x, x, _choice("block", block, "row", "tile"), rows, cols, dtype, scale_dtype,
+                 q, s, qt, st)
 
 
 def gemm_fp8(A, A_scales, B, B_scales, out=None, out_dtype=torch.bfloat16, accumulate=False, workspace=None,
@@ -303,85 +247,15 @@ def gemm_fp8(A, A_scales, B, B_scales, out=None, out_dtype=torch.bfloat16, accum
     contiguous with pitches a multiple of 16 bytes; scales fp32 or uint8 (UE8M0), both alike, [rows,
     ceil(K/128)] or, one per 128 rows, [ceil(rows/128), ceil(K/128)], of any strides.  Returns (out,
     workspace); the first int32 of the workspace is the device status once the stream has run the call."""
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError(f"A and B must be matrices, got shapes {tuple(A.shape)} and {tuple(B.shape)}")
-    M, K = A.shape
-    N = B.shape[0]
-    d = A.device
-    lda = _matrix("A", A, M, K, _FORMATS, d)
-    ldb = _matrix("B", B, N, K, _FORMATS, d)
-    kb = -(-K // 128)
-    if A_scales.dtype not in _SCALES:
-        raise TypeError(f"scales must be float32 or uint8 (UE8M0), got {A_scales.dtype}")
-    ar = _scale_rows("A_scales", A_scales, M, kb, A_scales.dtype, d)
-    br = _scale_rows("B_scales", B_scales, N, kb, A_scales.dtype, d)
-    if accumulate and out is None:
-        raise ValueError("accumulate needs the out to add to")
-    odt = out_dtype if out is None else out.dtype
-    if odt is not torch.bfloat16 and odt is not torch.float32:
-        raise TypeError(f"out must be bfloat16 or float32, got {odt}")
-    ldo = N if out is None else _matrix("out", out, M, N, (odt,), d)
-
-    def call(sp):
-        o = torch.empty(M, N, dtype=odt, device=d) if out is None else out
-        ws = torch.empty(256, dtype=torch.uint8, device=d) if workspace is None else workspace
-        rc = lib().moe_gemm_fp8(M, N, K, A.data_ptr(), lda, _FORMATS[A.dtype], A_scales.data_ptr(),
-                                *A_scales.stride(), ar, B.data_ptr(), ldb, _FORMATS[B.dtype], B_scales.data_ptr(),
-                                *B_scales.stride(), br, _SCALES[A_scales.dtype], o.data_ptr(), ldo, _TYPES[odt],
-                                accumulate, _ptr(ws, torch.uint8, d), ws.numel(), sp)
-        _check(rc, "moe_gemm_fp8")
-        return o, ws
-
-    return _run(d, stream, call)
-
-
-def _balance_args(logits, offsets, mask, score):
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [T, E], got shape {tuple(logits.shape)}")
-    T, E = logits.shape
-    d = logits.device
-    ldl = _matrix("logits", logits, T, E, (torch.float32, torch.bfloat16), d)
-    if score not in _SCORES:
-        raise ValueError(f"score must be one of {list(_SCORES)}, got {score!r}")
-    S, op, mp = 1, None, None
-    if offsets is not None:
-        if offsets.dim() != 1 or offsets.numel() < 2:
-            raise ValueError(f"offsets must be [S + 1], got shape {tuple(offsets.shape)}")
-        S, op = offsets.numel() - 1, _ptr(offsets, torch.int32, d)
-    if mask is not None:
-        if mask.shape != (T,):
-            raise ValueError(f"mask must be [{T}], got shape {tuple(mask.shape)}")
-        mp = _ptr(mask, torch.uint8 if mask.dtype == torch.uint8 else torch.bool, d)
-    return T, E, S, d, ldl, op, mp
+    return _call("gemm_fp8", stream, A, A, A_scales, B, B_scales, out, out_dtype, accumulate, workspace)
 
 
 def balance_loss(logits, topk_ids, coef=1.0, offsets=None, mask=None, score="softmax", workspace=None, stream=None):
     """Balance loss of the router through moe_balance_loss: logits [T, E] (fp32 or bf16), topk_ids int32
     [T, k], optionally offsets int32 [S + 1] of packed sequences and mask bool [T] of the tokens that count.
     Returns (loss fp32 [], counts int32 [S, E], probs fp32 [S, E], tokens int32 [S])."""
-    T, E, S, d, ldl, op, mp = _balance_args(logits, offsets, mask, score)
-    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
-        raise ValueError(f"topk_ids must be [{T}, k], got shape {tuple(topk_ids.shape)}")
-    k = topk_ids.shape[1]
-    ids = _ptr(topk_ids, torch.int32, d)
-    L = lib()
-    need = L.moe_balance_workspace_bytes(T, E, S)
-    if need == 0:
-        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_balance_workspace_bytes")
-
-    def call(sp):
-        ws = torch.empty(need, dtype=torch.uint8, device=d) if workspace is None else workspace
-        loss = torch.empty((), dtype=torch.float32, device=d)
-        counts = torch.empty(S, E, dtype=torch.int32, device=d)
-        probs = torch.empty(S, E, dtype=torch.float32, device=d)
-        tokens = torch.empty(S, dtype=torch.int32, device=d)
-        rc = L.moe_balance_loss(T, E, k, S, logits.data_ptr(), ldl, _TYPES[logits.dtype], ids, op, mp, _SCORES[score],
-                                coef, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(),
-                                _ptr(ws, torch.uint8, d), ws.numel(), sp)
-        _check(rc, "moe_balance_loss")
-        return loss, counts, probs, tokens
-
-    return _run(d, stream, call)
+    return _call("balance_loss", stream, logits, logits, topk_ids, coef, offsets, mask,
+                 _choice("score", score, "softmax", "sigmoid"), workspace)
 
 
 def balance_loss_backward(grad_loss, logits, counts, tokens, k: int, coef=1.0, offsets=None, mask=None,
@@ -389,23 +263,8 @@ def balance_loss_backward(grad_loss, logits, counts, tokens, k: int, coef=1.0, o
     """Gradient of grad_loss * balance_loss(...) with respect to the logits, through
     moe_balance_loss_backward: counts and tokens as balance_loss returned them, the other arguments as it
     got them.  Returns grad [T, E] of the logits' dtype (`out`; added to it with `accumulate`)."""
-    T, E, S, d, ldl, op, mp = _balance_args(logits, offsets, mask, score)
-    if grad_loss.numel() != 1 or counts.shape != (S, E) or tokens.shape != (S,):
-        raise ValueError(f"expected grad_loss [], counts [{S}, {E}] and tokens [{S}], got shapes "
-                         f"{tuple(grad_loss.shape)}, {tuple(counts.shape)} and {tuple(tokens.shape)}")
-    gp, cp, np_ = _ptr(grad_loss, torch.float32, d), _ptr(counts, torch.int32, d), _ptr(tokens, torch.int32, d)
-    if accumulate and out is None:
-        raise ValueError("accumulate needs the out to add to")
-    ldg = E if out is None else _matrix("out", out, T, E, (logits.dtype,), d)
-
-    def call(sp):
-        g = torch.empty(T, E, dtype=logits.dtype, device=d) if out is None else out
-        rc = lib().moe_balance_loss_backward(T, E, k, S, gp, logits.data_ptr(), ldl, _TYPES[logits.dtype], cp, np_,
-                                             op, mp, _SCORES[score], coef, g.data_ptr(), ldg, accumulate, sp)
-        _check(rc, "moe_balance_loss_backward")
-        return g
-
-    return _run(d, stream, call)
+    return _call("balance_loss_backward", stream, logits, grad_loss, logits, counts, tokens, k, coef, offsets, mask,
+                 _choice("score", score, "softmax", "sigmoid"), out, accumulate)
 
 
 def route_noalloc(x, W_router, bias, k: int, topk_ids=None, gates=None, stream=None):

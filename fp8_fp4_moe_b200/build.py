@@ -1,4 +1,5 @@
-"""Build libmoe_b200.so in-tree for sm_100a with nvcc.
+"""Build libmoe_b200.so in-tree for sm_100a with nvcc, and the native part of its Python binding
+(_moe_ops.so, against the installed torch) with g++.
 
     python -m fp8_fp4_moe_b200.build [--force] [--verbose]
 
@@ -19,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_b200.so")
+OPS = os.path.join(PKG, "_moe_ops.so")
+OPS_SOURCE = "ops_binding.cpp"
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["gemm_sm100.cu", "path_kernels.cu", "moe_api.cu", "noalloc.cu", "dense_api.cu", "gemm_fp8.cu", "quant_fp8.cu",
            "balance.cu"]
@@ -72,7 +75,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
+    build_ops(force, verbose)
     return LIB
+
+
+def build_ops(force: bool = False, verbose: bool = False) -> str:
+    """Compile the native part of the binding; it finds libmoe_b200.so beside itself, torch's libraries in
+    the process that imported torch."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, OPS_SOURCE)
+    if not force and not _stale(OPS, [src, os.path.join(INCLUDE, "moe_b200.h")]):
+        return OPS
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    at = os.path.dirname(torch.__file__)
+    inc = ["-I" + p for p in [INCLUDE, sysconfig.get_path("include"), os.path.join(cuda, "include"),
+                              os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include")]]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *inc, src, "-o", OPS,
+           "-L" + PKG, "-lmoe_b200", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed: {' '.join(cmd)}")
+    return OPS
 
 
 if __name__ == "__main__":
