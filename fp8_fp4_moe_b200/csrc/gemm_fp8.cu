@@ -508,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
       }
     } else if (warp == 1) {
-      if (rank == 0) {                 // the whole warp, one elected thread issues: the operands stay uniform
+      if (rank == 0 && elect()) {      // one thread; elected, so that the compiler keeps the operands uniform
         const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
         const uint64_t sp0 = sf_desc(smem_u32(smem + C::sfp)), sq0 = sf_desc(smem_u32(smem + C::sfq));
         int stage = 0, buf = 0, sf = 0;
@@ -516,50 +516,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
           for (int kb = 0; kb < KB; ++kb) {
-            if (!MX || kb == 0) ok = wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma);
-            if (MX && ok && (kb & 3) == 0) ok = wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2);
-            ok = ok && wait_for(&full[stage], phase, ctl, kWhereMma + 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if ((!MX || kb == 0) && !wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma)) { ok = false; break; }
+            if (MX && (kb & 3) == 0) {
+              if (!wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2)) { ok = false; break; }
+              tc_fence_after();
+              tsp = tmem + sf_col + sf * 16;     // the slots' columns alternate as well
+              const uint64_t sp = sp0 + sf * (512 >> 4), sq = sq0 + sf * (C::kSfq >> 4);
+              tc_cp_32x128b_warpx4_pair(tsp, sp);
+              tc_cp_32x128b_warpx4_pair(tsp + 4, sq);
+              tc_cp_32x128b_warpx4_pair(tsp + 8, sq + 32);
+              tc_commit_pair(&sempty[sf], 0x3);
+              if (++sf == kSfSlots) { sf = 0; sphase ^= 1; }
+            }
+            if (!wait_for(&full[stage], phase, ctl, kWhereMma + 1)) { ok = false; break; }
             tc_fence_after();
             const uint32_t acc = tmem + buf * acc_cols;
             const uint64_t dp = dp0 + stage * (kPBytes >> 4), dq = dq0 + stage * (C::kQBytes >> 4);
-            if (MX && (kb & 3) == 0) {
-              tsp = tmem + sf_col + sf * 16;     // the slots' columns alternate as well
-              if (elect()) {
-                const uint64_t sp = sp0 + sf * (512 >> 4), sq = sq0 + sf * (C::kSfq >> 4);
-                tc_cp_32x128b_warpx4_pair(tsp, sp);
-                tc_cp_32x128b_warpx4_pair(tsp + 4, sq);
-                tc_cp_32x128b_warpx4_pair(tsp + 8, sq + 32);
-                tc_commit_pair(&sempty[sf], 0x3);
-              }
-              __syncwarp();
-              if (++sf == kSfSlots) { sf = 0; sphase ^= 1; }
-            }
-            if (elect()) {
-              if constexpr (MX) {
-                const uint32_t id = with_byte(p.idesc, kb & 3);
+            if constexpr (MX) {
+              const uint32_t id = with_byte(p.idesc, kb & 3);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  tc_mma_mxf8f6f4_pair(acc, dp + 2 * i, dq + 2 * i, id, tsp, tsp + 4, kb | i);
-              } else {
+              for (int i = 0; i < 4; ++i) tc_mma_mxf8f6f4_pair(acc, dp + 2 * i, dq + 2 * i, id, tsp, tsp + 4, kb | i);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tc_mma_f8f6f4_pair(acc, dp + 2 * i, dq + 2 * i, p.idesc, i);
-              }
-              tc_commit_pair(&empty[stage], 0x3);
-              if (!MX || kb == KB - 1) tc_commit_pair(&accf[buf], 0x3);
+              for (int i = 0; i < 4; ++i) tc_mma_f8f6f4_pair(acc, dp + 2 * i, dq + 2 * i, p.idesc, i);
             }
-            __syncwarp();
+            tc_commit_pair(&empty[stage], 0x3);
             if (!MX || kb == KB - 1) {
+              tc_commit_pair(&accf[buf], 0x3);
               if (++buf == na) { buf = 0; aphase ^= 1; }
             }
             if (++stage == ST) { stage = 0; phase ^= 1; }
           }
         }
-        if (elect()) {
-          tc_commit_pair(drain, 0x1);
-          if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
-        }
+        tc_commit_pair(drain, 0x1);
+        if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
       }
     } else {
       auto feed = [&](auto sf) {
@@ -800,34 +790,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // the whole warp, one elected thread issues: the operands stay uniform
-    const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
-    const uint64_t sp0 = sf_desc(smem_u32(smem + C::sfp)), sq0 = sf_desc(smem_u32(smem + C::sfq));
-    int stage = 0, buf = 0, sf = 0;
-    uint32_t phase = 0, aphase = 0, sphase = 0, tsp = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int j = (kb - kb0) & 3;
-        if (!MX || kb == kb0) ok = wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma);
-        if (MX && ok && j == 0) ok = wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2);
-        ok = ok && wait_for(&full[stage], phase, ctl, kWhereMma + 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t acc = tmem + buf * BN;
-        const uint64_t dp = dp0 + stage * (kPBytes >> 4), dq = dq0 + stage * (C::kQBytes >> 4);
-        if (MX && j == 0) {
-          tsp = tmem + C::kSfCol + sf * 16;      // the slots' columns alternate as well
-          if (elect()) {
+    if (elect()) {                     // one thread; elected, so that the compiler keeps the operands uniform
+      const uint64_t dp0 = sw128(smem_u32(smem + C::p)), dq0 = sw128(smem_u32(smem + C::q));
+      const uint64_t sp0 = sf_desc(smem_u32(smem + C::sfp)), sq0 = sf_desc(smem_u32(smem + C::sfq));
+      int stage = 0, buf = 0, sf = 0;
+      uint32_t phase = 0, aphase = 0, sphase = 0, tsp = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x / S; tile < tiles && ok; tile += step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int j = kb & 3;                  // kb0 is a multiple of four
+          if ((!MX || kb == kb0) && !wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma)) { ok = false; break; }
+          if (MX && j == 0) {
+            if (!wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2)) { ok = false; break; }
+            tc_fence_after();
+            tsp = tmem + C::kSfCol + sf * 16;    // the slots' columns alternate as well
             tc_cp_32x128b_warpx4(tsp, sp0 + sf * (512 >> 4));
             tc_cp_32x128b_warpx4(tsp + 4, sq0 + sf * (C::kSfq >> 4));
             tc_commit(&sempty[sf]);
+            if (++sf == kSfSlots) { sf = 0; sphase ^= 1; }
           }
-          __syncwarp();
-          if (++sf == kSfSlots) { sf = 0; sphase ^= 1; }
-        }
-        if (elect()) {
+          if (!wait_for(&full[stage], phase, ctl, kWhereMma + 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t acc = tmem + buf * BN;
+          const uint64_t dp = dp0 + stage * (kPBytes >> 4), dq = dq0 + stage * (C::kQBytes >> 4);
           if constexpr (MX) {
             const uint32_t id = with_byte(p.idesc, j);
 #pragma unroll
@@ -837,16 +822,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             for (int i = 0; i < 4; ++i) tc_mma_f8f6f4(acc, dp + 2 * i, dq + 2 * i, p.idesc, i);
           }
           tc_commit(&empty[stage]);
-          if (!MX || kb == kb1 - 1) tc_commit(&accf[buf]);
+          if (!MX || kb == kb1 - 1) {
+            tc_commit(&accf[buf]);
+            if (++buf == NA) { buf = 0; aphase ^= 1; }
+          }
+          if (++stage == ST) { stage = 0; phase ^= 1; }
         }
-        __syncwarp();
-        if (!MX || kb == kb1 - 1) {
-          if (++buf == NA) { buf = 0; aphase ^= 1; }
-        }
-        if (++stage == ST) { stage = 0; phase ^= 1; }
       }
-    }
-    if (elect()) {
       tc_commit(drain);
       if (!mbar_wait_drain(drain, 0, p.timeout_ns)) report_status(p.status, kStatusTimeout, kWhereDrain, 99);
     }
@@ -1090,42 +1072,43 @@ struct Cut {
 
 int up(long a, long b) { return (int)((a + b - 1) / b); }
 
-Cut choose(int M, int N, int KB, int sms, bool b_tiled, bool mx) {
-  Cut c{false, M <= 128, 128, 1};
-  if (c.swap) {
-    c.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  } else {
-    // columns of a pair tile: the fewest clocks of the busiest pair (2 bn a K block, and about 40 K blocks' worth
-    // of columns for a tile's start and end), wide tiles on a tie
-    const int pairs = sms / 2;
-    long best = -1;
+// The cut with the least estimated time.  The estimates (microseconds) are a straight line through what the
+// kernels measured on B200 for a K block (128 deep) of one tile, at K of 2048 to 8192:
+//   pair    UE8M0 256 columns 0.45, 128 columns 0.29; fp32 0.57 and 0.35, column scales 0.82 and 0.53; 2 to start
+//   small   UE8M0 0.25 to 0.30, fp32 0.26 to 0.50; adding up a split tile 1.5 and its size
+// and not less than reading both operands once at 6.2 TB/s.  M = 256, N = 7168, K = 2048, UE8M0: small 8.7, pair
+// 11.2 us; M = 8192, N = 4096, K = 7168: pair 170, single CTAs of 256 columns 226 us; M = 1, N = 7168, K = 2048:
+// split in two 7.2, not split 8.3 us.
+Cut choose(int M, int N, int KB, int sms, bool qrow, bool mx) {
+  Cut best{false, M <= 128, 128, 1};
+  double least = 1e30;
+  const double memory = ((double)M + N) * KB * 128 / 6.2e6;
+  auto offer = [&](const Cut& c, double blocks, double block_us, double more) {
+    const double busy = blocks * block_us, t = (busy > memory ? busy : memory) + more;
+    if (t < least) {
+      least = t;
+      best = c;
+    }
+  };
+  // small: few tokens as columns (swapped), or 128 x 128 tiles
+  static const double kMx[4] = {0.245, 0.245, 0.262, 0.300}, kF32[4] = {0.256, 0.260, 0.349, 0.500};
+  const bool swap = M <= 128;
+  for (int i = swap ? 0 : 3, bn = swap ? 16 : 128; bn <= 128; bn *= 2, ++i) {
+    const long tiles = (long)up(swap ? N : M, 128) * up(swap ? M : N, bn);
+    for (int s = 1; s <= 8; s *= 2) {
+      if (s > 1 && (tiles * s > sms || KB < s * 4)) break;         // every part a group of four blocks at least
+      offer(Cut{false, swap, bn, s}, (double)((tiles * s + sms - 1) / sms) * up(KB, s), mx ? kMx[i] : kF32[i],
+            s > 1 ? 1.5 + 0.012 * bn : 0.0);
+    }
+  }
+  if (!swap)
     for (int bn = 256; bn >= 64; bn -= 32) {
-      if (!mx && bn != 256 && bn != 128) continue;       // the widths compiled for fp32 scales
-      const long waves = up((long)up(M, 256) * up(N, bn), pairs);
-      const long cost = waves * ((long)KB * (bn > 96 ? bn : 96) + 512);
-      if (best < 0 || cost < best) {
-        best = cost;
-        c.bn = bn;
-        c.pair = true;
-      }
+      if (!mx && bn != 256 && bn != 128) continue;                 // the widths compiled for fp32 scales
+      const double waves = (double)up((long)up(M, 256) * up(N, bn), sms / 2);
+      const double block = mx ? 0.130 + 0.00124 * bn : qrow ? 0.231 + 0.0023 * bn : 0.131 + 0.00172 * bn;
+      offer(Cut{true, false, bn, 1}, waves * KB, block, 2.0 + 0.3 * waves);
     }
-    // few tiles: the small kernel with the K loop split
-    const long t = (long)up(M, 128) * up(N, 128);
-    if (t * 2 <= sms && KB >= 8) {
-      int s = 1;
-      while (s < 8 && t * s * 2 <= sms && KB >= s * 8) s *= 2;
-      const long cost = (long)up(KB, s) * 192 + 1024;
-      if (cost < best) {
-        c.pair = false;
-        c.bn = 128;
-      }
-    }
-  }
-  if (!c.pair) {
-    const long t = (long)up(c.swap ? N : M, 128) * up(c.swap ? M : N, c.bn);
-    while (c.splits < 8 && t * c.splits * 2 <= sms && KB >= c.splits * 8) c.splits *= 2;   // a group of 4 or more each
-  }
-  return c;
+  return best;
 }
 
 }  // namespace
@@ -1169,7 +1152,7 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
 
   Fp8Args a{};
   a.KB = up(K, 128);
-  const Cut c = choose(M, N, a.KB, sms, b_scale_rows == 128, mx);
+  const Cut c = choose(M, N, a.KB, sms, b_scale_rows == 1, mx);
   a.swap = c.swap;
   a.splits = c.splits;
   a.bn = c.bn;
