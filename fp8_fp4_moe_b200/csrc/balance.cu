@@ -25,7 +25,7 @@ constexpr int kWarps = 8;
 
 struct BalanceArgs {
   int T, E, k, S, chunk, chunks, score;
-  int one_launch;            // the cluster kernel did everything
+  int clusters;              // the cluster kernel does the sums
   const void* logits;
   long ldl;
   const int32_t* ids;        // [T, k]
@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_part_kernel(const Bala
   }
 }
 
-// One sequence of few tokens: the blocks of one cluster have a share of the tokens each, then of the experts, whose
-// sums they add up in rank order through distributed shared memory.  One launch instead of two.
+// Few tokens: the blocks of a cluster have a share of a sequence's tokens each, then of the experts, whose sums they
+// add up in rank order through distributed shared memory.  One launch instead of two for one sequence.
 constexpr int kCluster = 8;
-constexpr int kClusterRounds = 8;      // rounds of rows a block of the cluster takes at most
+constexpr int kClusterRounds = 4;      // rounds of rows (0.9 us each) a block of the cluster takes at most
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -303,8 +303,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWarps * 32, 
   __shared__ int n_s;
   __shared__ double part_s[kCluster];
   __shared__ double warp_s[kWarps];
-  const int rank = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int a = min(p.T, rank * p.chunk), b = min(p.T, a + p.chunk);
+  const int rank = blockIdx.x % kCluster, s = blockIdx.x / kCluster, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Starts start{p.offsets, p.S, p.T};   // one look each
+  const int first = start[s], len = max(0, start[s + 1] - first), chunk = (len + kCluster - 1) / kCluster;
+  const int a = first + min(len, rank * chunk), b = first + min(len, (rank + 1) * chunk);
+  griddep_launch_dependents();         // the total's block may wait on the device already
   sum_tokens<T, LPR, J, V, U>(p, a, b, sum_s, cnt_s, n_s);
   for (int e = threadIdx.x; e < p.E; e += kWarps * 32) sum_s[e] = warps_sum(p, sum_s, e);   // column e is this thread's
   __syncthreads();
@@ -323,8 +326,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWarps * 32, 
       c += (int)ld_cluster(mapa_shared(cnt_s + e, r));
     }
     const float mean = n > 0 ? sum / inv : 0.f;
-    p.counts[e] = c;
-    p.probs[e] = mean;
+    p.counts[(long)s * p.E + e] = c;
+    p.probs[(long)s * p.E + e] = mean;
     v += (double)c * (double)mean;
   }
 #pragma unroll
@@ -343,14 +346,52 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWarps * 32, 
     v = 0.0;
 #pragma unroll
     for (int r = 0; r < kCluster; ++r) v += part_s[r];
-    p.tokens[0] = n;
-    *p.loss = n > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)n)) : 0.f;
+    p.tokens[s] = n;
+    if (p.S > 1) p.part_l[s] = n > 0 ? v / (double)n : 0.0;
+    if (p.S == 1) *p.loss = n > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)n * (double)n)) : 0.f;
   }
+}
+
+// The loss from n terms of the sequences, in 64 bits and a fixed order, by the threads of one block of kTotal warps.
+constexpr int kTotal = 8;
+__device__ __forceinline__ void write_total(const BalanceArgs& p, int n) {
+  __shared__ double v_s[kTotal];
+  __shared__ int live_s[kTotal];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double v = 0.0;
+  int live = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kTotal * 32) v += __ldcg(p.part_l + i);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.S; i += kTotal * 32) live += __ldcg(p.tokens + i) > 0;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) {
+    v_s[warp] = v;
+    live_s[warp] = live;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = 0.0;
+    live = 0;
+#pragma unroll
+    for (int w = 0; w < kTotal; ++w) {
+      v += v_s[w];
+      live += live_s[w];
+    }
+    *p.loss = live > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)live)) : 0.f;
+  }
+}
+__global__ void __launch_bounds__(kTotal * 32) balance_total_kernel(const BalanceArgs p) {
+  griddep_wait();
+  write_total(p, p.S);
 }
 
 // One block per (sequence, 8 experts): the slots of the sequence added up in order, every 32nd by one thread.
 // The last block of the grid adds up the loss.
 constexpr int kJoin = 32;
+static_assert(kJoin * 8 == kTotal * 32, "the join kernel's last block writes the total");
 __global__ void __launch_bounds__(kJoin * 8) balance_join_kernel(const BalanceArgs p) {
   __shared__ float fp[kJoin][8];
   __shared__ int fc[kJoin][8];
@@ -404,34 +445,7 @@ __global__ void __launch_bounds__(kJoin * 8) balance_join_kernel(const BalanceAr
   }
   __syncthreads();
   if (!last) return;
-  // the loss, in 64 bits: terms of one sign, in a fixed order
-  double v = 0.0;
-  int live = 0;
-  const int terms = gridDim.x * gridDim.y;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < terms; i += kJoin * 8) v += __ldcg(p.part_l + i);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < p.S; i += kJoin * 8) live += __ldcg(p.tokens + i) > 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  live = __reduce_add_sync(0xffffffffu, live);
-  __shared__ double lv[kJoin / 4];
-  if (lane == 0) {
-    lv[warp] = v;
-    fn[warp] = live;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    v = 0.0;
-    live = 0;
-#pragma unroll
-    for (int i = 0; i < kJoin / 4; ++i) {
-      v += lv[i];
-      live += fn[i];
-    }
-    *p.loss = live > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)live)) : 0.f;
-  }
+  write_total(p, gridDim.x * gridDim.y);
 }
 
 // Tokens outside every sequence and masked tokens get zeros (or stay, accumulating).
@@ -441,14 +455,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
   __shared__ int live_s;
   __shared__ int32_t starts_s[kStarts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) live_s = 0;
   const Starts start = stage_starts(p, starts_s);
-  __syncthreads();
-  int alive = 0;
-  for (int s = threadIdx.x; s < p.S; s += kWarps * 32) alive += p.tokens[s] > 0;
-  if (alive) atomicAdd(&live_s, alive);
-  __syncthreads();
-  const float base = *p.grad_loss * p.coef * (float)p.E / ((float)p.k * (float)max(1, live_s));
+  const float grad_loss = __ldg(p.grad_loss);
+  int live = 1;                        // sequences with tokens that count
+  if (p.offsets != nullptr) {
+    int alive = 0;
+    for (int s = threadIdx.x; s < p.S; s += kWarps * 32) alive += p.tokens[s] > 0;
+    if (threadIdx.x == 0) live_s = 0;
+    __syncthreads();
+    if (alive) atomicAdd(&live_s, alive);
+    __syncthreads();
+    live = max(1, live_s);
+  }
   const int step = gridDim.x * kWarps * Map::kRows;
   int have = -1;                       // the sequence that c and g are of
   float c[J], g = 0.f;
@@ -487,7 +505,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
           c[j] = e < p.E ? (float)__ldg(cs + e) : 0.f;
         }
         const float n = (float)max(1, p.tokens[have]);
-        g = base / n / n;
+        g = grad_loss * p.coef * (float)p.E / ((float)p.k * (float)live) / n / n;
       }
       const float z = scores<LPR, J>(p.score, seq[u] >= 0, l[u]);
       float mean = 0.f;
@@ -583,10 +601,15 @@ cudaError_t launch_as(BalanceArgs& a, bool grad, cudaStream_t s) {
     return cudaGetLastError();
   }
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4;
-  a.one_launch = a.offsets == nullptr && a.T <= kCluster * round * kClusterRounds;
-  if (a.one_launch) {
-    a.chunk = (a.T + kCluster - 1) / kCluster;
-    balance_cluster_kernel<T, LPR, J, V, U><<<kCluster, kWarps * 32, smem, s>>>(a);
+  // One sequence: up to the rounds at which two launches, on all SMs, are as fast (T = 512: 7.3 us; 2048: 12.7, two
+  // launches 8.5).  Several: a block of the two
+  // launches takes about 4 us for each sequence of its chunk, one after the other; clusters take 5 us and 0.135 us
+  // for each sequence over what fits the SMs (T = 16, S = 57: 79 us by chunks; T = 8191, S = 13: 22 us by chunks, 25
+  // by clusters).
+  a.clusters = a.S == 1 ? a.T <= kCluster * round * kClusterRounds
+                        : 4.0 * a.chunk * a.S / a.T > 5.0 + 0.135 * a.S;
+  if (a.clusters) {
+    balance_cluster_kernel<T, LPR, J, V, U><<<a.S * kCluster, kWarps * 32, smem, s>>>(a);
   } else {
     balance_part_kernel<T, LPR, J, V, U><<<a.chunks, kWarps * 32, smem, s>>>(a);
   }
@@ -665,10 +688,10 @@ int moe_balance_loss(int T, int E, int k, int S, const void* logits, long long l
   cudaError_t e = logits_type == MOE_TYPE_FP32 ? launch_any<float>(a, vec, false, s)
                                                : launch_any<__nv_bfloat16>(a, vec, false, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  if (a.one_launch) return MOE_OK;
+  if (a.clusters && S == 1) return MOE_OK;
   // a programmatic dependent: its blocks are placed while the first kernel ends (griddep_wait)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(S, (E + 7) / 8);
+  cfg.gridDim = a.clusters ? dim3(1) : dim3(S, (E + 7) / 8);
   cfg.blockDim = dim3(kJoin * 8);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -676,7 +699,8 @@ int moe_balance_loss(int T, int E, int k, int S, const void* logits, long long l
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  e = cudaLaunchKernelEx(&cfg, a.clusters ? balance_total_kernel : balance_join_kernel, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int moe_balance_loss_backward(int T, int E, int k, int S, const float* grad_loss, const void* logits, long long ldl,
