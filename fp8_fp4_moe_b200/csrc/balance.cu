@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWarps * 32, 
     for (int r = 0; r < kCluster; ++r) v += part_s[r];
     p.tokens[s] = n;
     if (p.S > 1) p.part_l[s] = n > 0 ? v / (double)n : 0.0;
-    if (p.S == 1) *p.loss = n > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)n * (double)n)) : 0.f;
+    if (p.S == 1) *p.loss = n > 0 ? (float)(v * (double)p.coef * (double)p.E / ((double)p.k * (double)n)) : 0.f;
   }
 }
 
