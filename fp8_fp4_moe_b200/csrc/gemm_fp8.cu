@@ -30,6 +30,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/moe_b200.h"
 #include "common.cuh"
@@ -342,29 +343,45 @@ __device__ __forceinline__ void store_frags(const Fp8Args& p, uint8_t* buf, cons
 // while the current ones wait for their slot.
 // UE8M0: an atom's word holds a row's scales of the four blocks; the MMAs of block j take byte j of it for all of
 // their 32-K steps, so that one copy to TMEM serves four blocks.  fp32: per block, [128] of P, then of Q.
+// The addresses are kept and advanced: worked out anew for each group, they took one warp longer than the group's
+// MMAs.
 template <bool MX, int FIRST, int NR, bool QROW>
 struct ScaleLoader {
+  using Word = std::conditional_t<MX, uint8_t, uint32_t>;
+  const Word* at[NR];                // scales of the next four blocks
+  uint32_t live;                     // items inside the matrix
+  bool quad[2];                      // P, Q: one load for four blocks (MX: v[i][0] is the atom's word then)
+  bool quads;                        // ... in what v holds
   uint32_t v[NR][4];
-  bool packed[2];                    // MX: v[i][0] is the word already (P, Q)
-  __device__ __forceinline__ void load(const Fp8Args& p, int p_row, int q_row, int q_n, int lane, int kb, int kb1) {
-    constexpr uint32_t kNone = MX ? 127u : 0u;   // past the matrix
-    packed[0] = packed[1] = false;
+  static __device__ __forceinline__ constexpr bool is_p(int i) { return FIRST + i < 4; }
+  __device__ __forceinline__ void begin(const Fp8Args& p, int p_row, int q_row, int q_n, int lane, int kb) {
+    live = 0;
+    quad[0] = p.sp_quad;
+    quad[1] = p.sq_quad;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const bool is_p = FIRST + i < 4;
-      const int in = is_p ? lane + 32 * (FIRST + i) : QROW ? lane + 32 * (FIRST + i - 4) : lane * 128, row = (is_p ? p_row : q_row) + in;
-      const bool live = is_p ? row < p.p_rows : in < q_n && row < p.q_rows;
-      const long blk = is_p ? p.sp_blk : p.sq_blk;
-      const long at = (is_p ? (long)(row >> p.sp_shift) * p.sp_row : (long)(row >> p.sq_shift) * p.sq_row) + kb * blk;
-      const bool quad = (is_p ? p.sp_quad : p.sq_quad) && kb + 4 <= kb1;
-      if (quad) {
+      const int in = is_p(i) ? lane + 32 * (FIRST + i) : QROW ? lane + 32 * (FIRST + i - 4) : lane * 128;
+      const int row = (is_p(i) ? p_row : q_row) + in;
+      const bool on = is_p(i) ? row < p.p_rows : in < q_n && row < p.q_rows;
+      const long o = is_p(i) ? (long)(row >> p.sp_shift) * p.sp_row + kb * p.sp_blk
+                             : (long)(row >> p.sq_shift) * p.sq_row + kb * p.sq_blk;
+      at[i] = static_cast<const Word*>(is_p(i) ? p.sp : p.sq) + (on ? o : 0);
+      live |= (uint32_t)on << i;
+    }
+  }
+  // the next n blocks (n <= 0: none), and on to the four after them
+  __device__ __forceinline__ void load(const Fp8Args& p, int n) {
+    constexpr uint32_t kNone = MX ? 127u : 0u;   // past the matrix
+    quads = n >= 4;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const bool on = live >> i & 1;
+      const long blk = is_p(i) ? p.sp_blk : p.sq_blk;
+      if (quads && quad[is_p(i) ? 0 : 1]) {
         if constexpr (MX) {
-          packed[is_p ? 0 : 1] = true;
-          v[i][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_p ? p.sp : p.sq) + at))
-                         : 0x7F7F7F7Fu;
+          v[i][0] = on ? __ldg(reinterpret_cast<const uint32_t*>(at[i])) : 0x7F7F7F7Fu;
         } else {
-          const uint4 w = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(is_p ? p.sp : p.sq) + at))
-                               : make_uint4(0, 0, 0, 0);
+          const uint4 w = on ? __ldg(reinterpret_cast<const uint4*>(at[i])) : make_uint4(0, 0, 0, 0);
           v[i][0] = w.x;
           v[i][1] = w.y;
           v[i][2] = w.z;
@@ -372,16 +389,9 @@ struct ScaleLoader {
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][j] = kNone;
-          if (live && kb + j < kb1) {
-            if constexpr (MX)
-              v[i][j] = __ldg(static_cast<const uint8_t*>(is_p ? p.sp : p.sq) + at + j * blk);
-            else
-              v[i][j] = __ldg(static_cast<const uint32_t*>(is_p ? p.sp : p.sq) + at + j * blk);
-          }
-        }
+        for (int j = 0; j < 4; ++j) v[i][j] = on && j < n ? __ldg(at[i] + j * blk) : kNone;
       }
+      if (on) at[i] += 4 * blk;
     }
   }
   __device__ __forceinline__ void store_atoms(uint8_t* sfp, uint8_t* sfq, int lane) {
@@ -390,7 +400,7 @@ struct ScaleLoader {
       uint32_t w[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        w[r] = packed[i < 4 ? 0 : 1] ? v[i + r][0] : v[i + r][0] | v[i + r][1] << 8 | v[i + r][2] << 16 | v[i + r][3] << 24;
+        w[r] = quads && quad[i < 4 ? 0 : 1] ? v[i + r][0] : v[i + r][0] | v[i + r][1] << 8 | v[i + r][2] << 16 | v[i + r][3] << 24;
       *reinterpret_cast<uint4*>((i < 4 ? sfp : sfq + (i - 4) * 128) + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     fence_proxy_async_smem();
@@ -560,7 +570,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           int tp, tq;
           tile_coord(p, tile, tp, tq);
           const int p_row = tp * 256 + rank * BM, q_row = tq * bn;
-          sf.load(p, p_row, q_row, bn, lane, 0, KB);
+          sf.begin(p, p_row, q_row, bn, lane, 0);
+          sf.load(p, KB);
           for (int kb = 0; kb < KB; kb += 4) {
             ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
             if (!ok) break;
@@ -571,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, lane);
               if (lane == 0) mbar_arrive(&sfull[slot]);
             }
-            sf.load(p, p_row, q_row, bn, lane, kb + 4, KB);
+            sf.load(p, KB - kb - 4);
             if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
           }
         }
@@ -840,7 +851,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       int tp, tq;
       tile_coord(p, tile, tp, tq);
       ScaleLoader<MX, 0, MX ? 8 : 4 + (BN + 31) / 32, true> sf;
-      sf.load(p, tp * BM, tq * BN, BN, lane, kb0, kb1);
+      sf.begin(p, tp * BM, tq * BN, BN, lane, kb0);
+      sf.load(p, kb1 - kb0);
       for (int kb = kb0; kb < kb1; kb += 4) {
         ok = __all_sync(0xffffffffu, wait_for(&sempty[slot], phase ^ 1, ctl, kWhereScales));
         if (!ok) break;
@@ -849,7 +861,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         else
           sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, lane);
         if (lane == 0) mbar_arrive(&sfull[slot]);
-        sf.load(p, tp * BM, tq * BN, BN, lane, kb + 4, kb1);
+        sf.load(p, kb1 - kb - 4);
         if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
       }
     }
