@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/moe_b200.h"
 #include "common.cuh"
@@ -86,20 +87,12 @@ struct Vec8 {
 };
 
 // E5 = E5M2 (largest value 1.75 * 2^15), else E4M3 (1.75 * 2^8): the exponent rule is the same one
-// shifted by the difference of the two largest exponents.
+// shifted by the difference of the two largest exponents.  A subnormal amax ends at the least exponent.
 template <bool E5>
 __device__ __forceinline__ int block_exp(float amax) {
-  if (!(amax > 0.f)) return 0;
   const uint32_t bits = __float_as_uint(amax);
-  int e = (int)(bits >> 23);
-  uint32_t man = bits & 0x7FFFFF;
-  if (e == 0) {                        // subnormal: normalise
-    const int lz = __clz(man) - 8;
-    man = (man << lz) & 0x7FFFFF;
-    e = 1 - lz;
-  }
-  const int p = e - 127 - (E5 ? 15 : 8) + (man > 0x600000u ? 1 : 0);
-  return p < -126 ? -126 : p;
+  const int p = (int)(bits >> 23) - 127 - (E5 ? 15 : 8) + ((bits & 0x7FFFFF) > 0x600000u ? 1 : 0);
+  return amax > 0.f ? max(p, -126) : 0;
 }
 
 template <bool E5>
@@ -131,10 +124,54 @@ __device__ __forceinline__ void store_codes8(uint8_t* dst, uint2 v, int n) {
     if (i < n) dst[i] = (uint8_t)((i < 4 ? v.x : v.y) >> ((i & 3) * 8));
 }
 
+// Scales as the elements are multiplied: bf16 in pairs as they are stored (a power of two changes the exponent
+// alone; what becomes subnormal is far below FP8's least value), the other types in fp32.
+struct Scale {
+  float f;
+  uint32_t h;                        // bf16 bits
+  __device__ __forceinline__ explicit Scale(int p = 0) : f(exp2_neg(p)), h((uint32_t)(127 - p) << 7) {}
+};
+// Words of two values a (first half) and b.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t v, uint32_t s) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&s));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
 template <class T, bool E5>
-__device__ __forceinline__ uint2 encode8(const Vec8<T>& v, float sc) {
-  return make_uint2(pack4<E5>(v.get(0) * sc, v.get(1) * sc, v.get(2) * sc, v.get(3) * sc),
-                    pack4<E5>(v.get(4) * sc, v.get(5) * sc, v.get(6) * sc, v.get(7) * sc));
+__device__ __forceinline__ uint2 encode8(const Vec8<T>& v, const Scale& sc) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = mul_bf16x2(v.w[i], sc.h * 0x10001u);
+    return make_uint2(pack4<E5>(low(w[0]), high(w[0]), low(w[1]), high(w[1])),
+                      pack4<E5>(low(w[2]), high(w[2]), low(w[3]), high(w[3])));
+  } else {
+    return make_uint2(pack4<E5>(v.get(0) * sc.f, v.get(1) * sc.f, v.get(2) * sc.f, v.get(3) * sc.f),
+                      pack4<E5>(v.get(4) * sc.f, v.get(5) * sc.f, v.get(6) * sc.f, v.get(7) * sc.f));
+  }
+}
+// Columns 2 j and 2 j + 1 of 8 rows, each with its scale.
+template <class T, bool E5>
+__device__ __forceinline__ void encode_columns(const Vec8<T> (&v)[8], int j, const Scale& a, const Scale& b, uint2 (&out)[2]) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = mul_bf16x2(v[i].w[j], a.h | b.h << 16);
+    out[0] = make_uint2(pack4<E5>(low(w[0]), low(w[1]), low(w[2]), low(w[3])),
+                        pack4<E5>(low(w[4]), low(w[5]), low(w[6]), low(w[7])));
+    out[1] = make_uint2(pack4<E5>(high(w[0]), high(w[1]), high(w[2]), high(w[3])),
+                        pack4<E5>(high(w[4]), high(w[5]), high(w[6]), high(w[7])));
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float s = h ? b.f : a.f;
+      const int c = 2 * j + h;
+      out[h] = make_uint2(pack4<E5>(v[0].get(c) * s, v[1].get(c) * s, v[2].get(c) * s, v[3].get(c) * s),
+                          pack4<E5>(v[4].get(c) * s, v[5].get(c) * s, v[6].get(c) * s, v[7].get(c) * s));
+    }
+  }
 }
 
 // Largest magnitudes; a NaN is passed over.  Two 16-bit values share an instruction: their magnitudes, with the
@@ -173,6 +210,34 @@ __device__ __forceinline__ float amax8(const Vec8<T>& v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) a = max2<T>(a, v.w[i]);
     return fmaxf(half_of<T>(a, 0), half_of<T>(a, 1));
+  }
+}
+// of the 8 rows, over the 16 lanes that share them
+template <class T>
+__device__ __forceinline__ void row_amax(const Vec8<T> (&v)[8], float (&a)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = amax8(v[i]);
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) a[i] = fmaxf(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {           // two rows to a word
+      uint32_t m[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m[h] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[h] = max2<T>(m[h], v[i + h].w[j]);
+      }
+      uint32_t w = max2<T>(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) w = max2<T>(w, __shfl_xor_sync(0xffffffffu, w, o));
+      a[i] = half_of<T>(w, 0);
+      a[i + 1] = half_of<T>(w, 1);
+    }
   }
 }
 // of each of the 8 columns of 8 rows
@@ -218,7 +283,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     const int e = block_exp<E5>(a);
-    store_codes8(p.q + row * p.ldq + k0, encode8<T, E5>(v, exp2_neg(e)), n);
+    store_codes8(p.q + row * p.ldq + k0, encode8<T, E5>(v, Scale(e)), n);
     if (live && l16 == 0) store_scale(p.s, row * p.s_row + blk * p.s_blk, e, p.ue8m0);
   }
 }
@@ -244,7 +309,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tile_kernel
     const int m = m0 + g * 8 + i;
     v[i].load(static_cast<const T*>(p.x) + (long)m * p.ldx + kc, m < p.M ? nk : 0, p.x_vec);
   }
-  float sc_tile = 1.f;
+  Scale sc_tile;
   if constexpr (TILE) {
     float a = 0.f;
 #pragma unroll
@@ -256,30 +321,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tile_kernel
 #pragma unroll
     for (int w = 0; w < 8; ++w) a = fmaxf(a, cmax[0][w]);
     const int e = block_exp<E5>(a);
-    sc_tile = exp2_neg(e);
+    sc_tile = Scale(e);
     if (tid == 0) {
       if (p.q) store_scale(p.s, blockIdx.y * p.s_row + blockIdx.x * p.s_blk, e, p.ue8m0);
       if (p.qt) store_scale(p.st, blockIdx.x * p.st_row + blockIdx.y * p.st_blk, e, p.ue8m0);
     }
   }
   if (p.q) {
+    float a[8];
+    if constexpr (!TILE) row_amax<T>(v, a);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int m = m0 + g * 8 + i;
-      float sc = sc_tile;
+      Scale sc = sc_tile;
       if constexpr (!TILE) {
-        float a = amax8(v[i]);
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const int e = block_exp<E5>(a);
-        sc = exp2_neg(e);
-        if (c == 0 && m < p.M) store_scale(p.s, (long)m * p.s_row + blockIdx.x * p.s_blk, e, p.ue8m0);
+        const int e = block_exp<E5>(a[i]);
+        sc = Scale(e);
+        if (c == i && m < p.M) store_scale(p.s, (long)m * p.s_row + blockIdx.x * p.s_blk, e, p.ue8m0);
       }
       if (m < p.M) store_codes8(p.q + (long)m * p.ldq + kc, encode8<T, E5>(v[i], sc), nk);
     }
   }
   if (!p.qt) return;
-  float sc[8];
+  Scale sc[8];
   if constexpr (TILE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sc[j] = sc_tile;
@@ -304,15 +368,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tile_kernel
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] = exp2_neg(cexp[c * 8 + j]);
+    for (int j = 0; j < 8; ++j) sc[j] = Scale(cexp[c * 8 + j]);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint2 w = make_uint2(
-        pack4<E5>(v[0].get(j) * sc[j], v[1].get(j) * sc[j], v[2].get(j) * sc[j], v[3].get(j) * sc[j]),
-        pack4<E5>(v[4].get(j) * sc[j], v[5].get(j) * sc[j], v[6].get(j) * sc[j], v[7].get(j) * sc[j]));
-    const int col = c * 8 + j;
-    *reinterpret_cast<uint2*>(tr + col * 128 + ((g ^ c) & 15) * 8) = w;
+  for (int j = 0; j < 4; ++j) {
+    uint2 w[2];
+    encode_columns<T, E5>(v, j, sc[2 * j], sc[2 * j + 1], w);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint2*>(tr + (c * 8 + 2 * j + h) * 128 + ((g ^ c) & 15) * 8) = w[h];
   }
   __syncthreads();
   // 16 lanes per transposed row, 8 bytes each; piece h of row `col` sits at h ^ (col / 8)
