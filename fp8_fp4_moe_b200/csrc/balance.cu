@@ -588,7 +588,7 @@ Layout layout(int T, int E, int S) {
 }
 
 bool shape_ok(int T, int E, int k, int S) {
-  return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= 16 && k <= E && S >= 1 && S <= (1 << 20);
+  return T >= 0 && T <= (1 << 30) && E >= 1 && E <= 1024 && k >= 1 && k <= 16 && k <= E && S >= 1 && S <= (1 << 20);
 }
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

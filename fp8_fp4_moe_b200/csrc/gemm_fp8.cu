@@ -1134,7 +1134,8 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
                  int b_format, const void* B_scales, long long bs_row_stride, long long bs_block_stride,
                  int b_scale_rows, int scale_type, void* out, long long ldo, int out_type, int accumulate,
                  void* workspace, size_t workspace_bytes, void* stream) {
-  if (M < 0 || N < 0 || K < 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // row and column numbers of the last tile stay in 32 bits; a K loop ends well inside the wait limit
+  if (M < 0 || N < 0 || K < 0 || M > (1 << 30) || N > (1 << 30) || K > (1 << 28)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if ((a_format != MOE_FP8_E4M3 && a_format != MOE_FP8_E5M2) || (b_format != MOE_FP8_E4M3 && b_format != MOE_FP8_E5M2) ||
       (scale_type != MOE_SCALE_FP32 && scale_type != MOE_SCALE_UE8M0) ||
       (out_type != MOE_TYPE_BF16 && out_type != MOE_TYPE_FP32) || (accumulate && out_type != MOE_TYPE_FP32) ||

@@ -375,7 +375,7 @@ enum moe_block {
  * M == 0 or K == 0 writes nothing.  Only the K (M) codes of a row are written, not its padding.
  * x, 16-byte aligned q and qt with pitches a multiple of 16 (one row: any pitch).  x may not overlap the
  * outputs.  Asynchronous on `stream`.  MOE_OK, MOE_ERR_INVALID_ARG (pointer, pitch, type),
- * MOE_ERR_UNSUPPORTED_SHAPE (negative; over 8,388,480 rows with tiles or qt) or MOE_ERR_CUDA. */
+ * MOE_ERR_UNSUPPORTED_SHAPE (negative; over 2^30; over 8,388,480 rows with tiles or qt) or MOE_ERR_CUDA. */
 int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_type, int block, int format, int scale_type,
                   void* q, long long ldq, void* scales, long long s_row_stride, long long s_block_stride, void* qt,
                   long long ldqt, void* scales_t, long long st_row_stride, long long st_block_stride, void* stream);
@@ -386,9 +386,11 @@ int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_type, int bl
  * scale_type; sA(m, b) = A_scales[(m / a_scale_rows) * as_row_stride + b * as_block_stride] with
  * a_scale_rows 1 or 128 (likewise B), so any order of the scale arrays is accepted; scales of
  * consecutive rows next to each other (row stride 1) load fastest.  out [M][N], row pitch ldo, is
- * bf16 or fp32 (out_type); accumulate (fp32 only) adds to it.  Products and sums are fp32 on the tensor
+ * bf16 or fp32 (out_type); accumulate (fp32 only) adds to it, one addition per element and call (sums
+ * below 2^-126 may become 0).  Products and sums are fp32 on the tensor
  * cores: UE8M0 scales are applied by the block-scaled MMA, fp32 scales (any finite value) to each K
- * block's fp32 sum outside it.  M, N, K >= 0, odd ones included; K == 0 gives zeros (or adds nothing).
+ * block's fp32 sum outside it.  0 <= M, N <= 2^30, 0 <= K <= 2^28, odd ones included; K == 0 gives
+ * zeros (or adds nothing).
  * A and B 16-byte aligned, lda and ldb multiples of 16 (one row: any pitch); out aligned to its type (16
  * bytes and a pitch of a multiple of 16 bytes store fastest); out may not overlap the operands.
  * `workspace`: 256-byte aligned, at least moe_gemm_fp8_workspace_bytes(), holds the status words in its
@@ -417,7 +419,7 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
  * not count (its logits are not read); NULL = all count.  A logit of -inf gives a score of 0, a row of
  * them scores of 0 throughout; NaN and +inf give NaN.  Outputs: loss fp32 [1], counts int32 [S][E], probs
  * fp32 [S][E], tokens int32 [S] (n_s).  Sums run in fp32 in a fixed order (the loss in fp64): results
- * repeat bit for bit.  Shapes: T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 2^20.
+ * repeat bit for bit.  Shapes: 0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 2^20.
  * Workspace: 256-byte aligned, moe_balance_workspace_bytes(T, E, S) (0 for an unsupported shape); calls
  * that may overlap on the device need their own.  Asynchronous on `stream`. */
 enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };

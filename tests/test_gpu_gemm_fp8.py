@@ -101,6 +101,38 @@ def test_exact_long_k(cuda_lib, M, N, K, kind, order):
     _equal(*binding.gemm_fp8(A, As, B, Bs, out_dtype=torch.float32), O.gemm(a, sa, b, sb)[0])
 
 
+@pytest.mark.parametrize("M,N,K", [(128, 30000, 256), (70, 9000, 400), (16, 40000, 130), (129, 128, 4096), (140, 20000, 128),
+                                   (2000, 64, 512), (4097, 1, 256), (1, 40001, 128), (600, 5000, 256)])
+@pytest.mark.parametrize("kind", ["fp32", "ue8m0"])
+def test_exact_cuts(cuda_lib, M, N, K, kind):
+    # sizes at which the tiles are cut in each of the ways: column tiles of 16 to 256, one and two CTAs, split K loops
+    rng = np.random.default_rng(M + N)
+    a, A = _codes(rng, M, K, "e4m3")
+    b, B = _codes(rng, N, K, "e4m3")
+    if K > 1100:                                         # codes of -1, 0 and 1
+        for v, t in ((a, A), (b, B)):
+            np.sign(v, out=v)
+            t.view(torch.uint8).copy_(torch.from_numpy(O.encode_fp8(v, "e4m3")))
+    for per in ("row", "tile"):
+        sa, As = _scales(rng, M, K, "row", kind)
+        sb, Bs = _scales(rng, N, K, per, kind)
+        x = torch.from_numpy(O.dequant(a, sa)).cuda()
+        y = torch.from_numpy(O.dequant(b, sb)).cuda()
+        _equal(*binding.gemm_fp8(A, As, B, Bs, out_dtype=torch.float32), (x @ y.T).cpu().numpy())
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_exact_random_sizes(cuda_lib, seed):
+    rng = np.random.default_rng(1000 + seed)
+    M, N, K = (int(np.exp(rng.uniform(0, np.log(top)))) for top in (1500, 3000, 1100))
+    kind, order = rng.choice(["fp32", "ue8m0"]), rng.choice(["rows", "columns"])
+    a_per, b_per = rng.choice(["row", "tile"]), rng.choice(["row", "tile"])
+    ref, *op = _case(seed, M, N, K, kind, a_per=a_per, b_per=b_per, fa=rng.choice(["e4m3", "e5m2"]),
+                     fb=rng.choice(["e4m3", "e5m2"]), order=order)
+    dtype = torch.float32 if rng.random() < 0.5 else torch.bfloat16
+    _equal(*binding.gemm_fp8(*op, out_dtype=dtype), ref)
+
+
 @pytest.mark.parametrize("M,N,K", [(9, 200, 300), (129, 260, 1024), (700, 513, 128)])
 @pytest.mark.parametrize("kind", ["fp32", "ue8m0"])
 def test_accumulate_strided_and_unaligned_outputs(cuda_lib, M, N, K, kind):

@@ -84,6 +84,28 @@ def test_special_values(cuda_lib, fmt, block, cols):
     _check(x.cuda(), fmt, block, True, cols, torch.uint8)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("block,cols", [("row", False), ("row", True), ("tile", True)])
+def test_special_16_bit_values(cuda_lib, dtype, fmt, block, cols):
+    i = torch.finfo(dtype)
+    x = _x(5, 140, 390, dtype)
+    x[0, :] = float("nan")
+    x[1, 7] = float("nan")
+    x[2, 130:140] = float("inf")
+    x[3, 200] = -float("inf")
+    x[4] = i.max
+    x[5] = i.min
+    x[6] = i.tiny
+    x[7] = i.tiny * 2.0 ** -6                            # subnormal
+    x[8] = i.smallest_normal * i.eps
+    x[9, 1:] = 0
+    x[10] = -0.0
+    x[:, 300] = float("nan")
+    x[:, 301] = 0
+    _check(x.cuda(), fmt, block, True, cols, torch.float32)
+
+
 def test_every_bf16_value_against_its_block(cuda_lib):
     # all finite bf16 values, each beside an amax that sets the scale: ties and the subnormal codes
     v = torch.arange(0, 0x7F80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)

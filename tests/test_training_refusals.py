@@ -25,7 +25,7 @@ QUANT = dict(M=4, K=200, x=P, ldx=200, x_type=0, block=0, format=0, scale_type=0
     ({"q": P + 8}, ARG), ({"ldq": 200}, ARG), ({"ldq": 192}, ARG), ({"scales": None}, ARG), ({"scales": P + 2}, ARG),
     ({"s_row": -1}, ARG), ({"s_blk": -1}, ARG), ({"qt": P + 4}, ARG), ({"ldqt": 8}, ARG), ({"ldqt": 0}, ARG),
     ({"scales_t": None}, ARG), ({"st_row": -1}, ARG), ({"st_blk": -1}, ARG),
-    ({"M": 65536 * 128, "ldqt": 65536 * 128}, SHAPE),
+    ({"M": 65536 * 128, "ldqt": 65536 * 128}, SHAPE), ({"M": (1 << 30) + 1}, SHAPE), ({"K": (1 << 30) + 1}, SHAPE),
 ])
 def test_quant_refuses(L, change, code):
     assert L.moe_quant_fp8(*(QUANT | change).values()) == code
@@ -42,6 +42,7 @@ GEMM = dict(M=4, N=8, K=200, A=P, lda=208, a_format=0, A_scales=P, as_row=1, as_
 
 
 @pytest.mark.parametrize("change,code", [
+    ({"M": (1 << 30) + 1}, SHAPE), ({"N": (1 << 30) + 1}, SHAPE), ({"K": (1 << 28) + 1}, SHAPE),
     ({"M": -1}, SHAPE), ({"N": -1}, SHAPE), ({"K": -1}, SHAPE), ({"a_format": 2}, ARG), ({"b_format": -1}, ARG),
     ({"scale_type": 2}, ARG), ({"out_type": 2}, ARG), ({"accumulate": 1}, ARG), ({"a_rows": 64}, ARG), ({"b_rows": 0}, ARG),
     ({"workspace": None}, WS), ({"workspace": P + 128}, WS), ({"bytes": 255}, WS), ({"out": None}, ARG), ({"out": P + 1}, ARG),
@@ -58,7 +59,7 @@ LOSS = dict(T=4, E=8, k=2, S=1, logits=P, ldl=8, type=1, ids=P, offsets=None, ma
 
 
 @pytest.mark.parametrize("change,code", [
-    ({"T": -1}, SHAPE), ({"E": 0}, SHAPE), ({"E": 1025, "ldl": 1025}, SHAPE), ({"k": 0}, SHAPE), ({"k": 9}, SHAPE),
+    ({"T": (1 << 30) + 1}, SHAPE), ({"T": -1}, SHAPE), ({"E": 0}, SHAPE), ({"E": 1025, "ldl": 1025}, SHAPE), ({"k": 0}, SHAPE), ({"k": 9}, SHAPE),
     ({"E": 32, "ldl": 32, "k": 17}, SHAPE), ({"S": 0}, SHAPE), ({"S": (1 << 20) + 1, "offsets": P}, SHAPE), ({"type": 2}, ARG),
     ({"score": 2}, ARG), ({"coef": float("nan")}, ARG), ({"coef": float("inf")}, ARG), ({"logits": None}, ARG),
     ({"logits": P + 2}, ARG), ({"ldl": 7}, ARG), ({"ids": None}, ARG), ({"ids": P + 2}, ARG), ({"S": 2}, ARG),
