@@ -265,10 +265,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_part_kernel(const Bala
   int* cnt_s = reinterpret_cast<int*>(sm + kWarps * p.E);   // [E]
   __shared__ int n_s;
   __shared__ int32_t starts_s[kStarts];
+  griddep_wait();
+  griddep_launch_dependents();         // the join kernel's blocks wait on the device
   const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   const Starts start = stage_starts(p, starts_s);
   __syncthreads();
-  griddep_launch_dependents();         // the join kernel's blocks may wait on the device already
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
   for (int s = max(0, start.of(t0)); s < p.S; ++s) {
     const int a = max(t0, start[s]), b = min(t1, start[s + 1]);
@@ -303,11 +304,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWarps * 32, 
   __shared__ int n_s;
   __shared__ double part_s[kCluster];
   __shared__ double warp_s[kWarps];
+  griddep_wait();
+  griddep_launch_dependents();         // the total's block waits on the device
   const int rank = blockIdx.x % kCluster, s = blockIdx.x / kCluster, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Starts start{p.offsets, p.S, p.T};   // one look each
   const int first = start[s], len = max(0, start[s + 1] - first), chunk = (len + kCluster - 1) / kCluster;
   const int a = first + min(len, rank * chunk), b = first + min(len, (rank + 1) * chunk);
-  griddep_launch_dependents();         // the total's block may wait on the device already
   sum_tokens<T, LPR, J, V, U>(p, a, b, sum_s, cnt_s, n_s);
   for (int e = threadIdx.x; e < p.E; e += kWarps * 32) sum_s[e] = warps_sum(p, sum_s, e);   // column e is this thread's
   __syncthreads();
@@ -385,6 +387,7 @@ __device__ __forceinline__ void write_total(const BalanceArgs& p, int n) {
 }
 __global__ void __launch_bounds__(kTotal * 32) balance_total_kernel(const BalanceArgs p) {
   griddep_wait();
+  griddep_launch_dependents();
   write_total(p, p.S);
 }
 
@@ -398,6 +401,7 @@ __global__ void __launch_bounds__(kJoin * 8) balance_join_kernel(const BalanceAr
   __shared__ int fn[kJoin];
   __shared__ bool last;
   griddep_wait();
+  griddep_launch_dependents();
   const int x = threadIdx.x & 7, w = threadIdx.x >> 3;
   const int s = blockIdx.x, e = blockIdx.y * 8 + x;
   const Starts start{p.offsets, p.S, p.T};
@@ -454,6 +458,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
   using Map = RowMap<T, LPR, J, V>;
   __shared__ int live_s;
   __shared__ int32_t starts_s[kStarts];
+  griddep_wait();
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Starts start = stage_starts(p, starts_s);
   const float grad_loss = __ldg(p.grad_loss);
@@ -597,8 +603,8 @@ cudaError_t launch_as(BalanceArgs& a, bool grad, cudaStream_t s) {
   const int round = kWarps * 32 / LPR * U;                  // tokens of a block a round
   if (grad) {
     const int need = (a.T + kWarps * 32 / LPR - 1) / (kWarps * 32 / LPR);
-    balance_grad_kernel<T, LPR, J, V, U><<<need < 2 * 148 ? need : 2 * 148, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(balance_grad_kernel<T, LPR, J, V, U>, dim3(need < 2 * 148 ? need : 2 * 148), kWarps * 32, 0, 1, s,
+                            a);
   }
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4;
   // One sequence: up to the rounds at which two launches, on all SMs, are as fast (T = 512: 7.3 us; 2048: 12.7, two
@@ -608,12 +614,9 @@ cudaError_t launch_as(BalanceArgs& a, bool grad, cudaStream_t s) {
   // by clusters).
   a.clusters = a.S == 1 ? a.T <= kCluster * round * kClusterRounds
                         : 4.0 * a.chunk * a.S / a.T > 5.0 + 0.135 * a.S;
-  if (a.clusters) {
-    balance_cluster_kernel<T, LPR, J, V, U><<<a.S * kCluster, kWarps * 32, smem, s>>>(a);
-  } else {
-    balance_part_kernel<T, LPR, J, V, U><<<a.chunks, kWarps * 32, smem, s>>>(a);
-  }
-  return cudaGetLastError();
+  return a.clusters
+             ? launch_dependent(balance_cluster_kernel<T, LPR, J, V, U>, dim3(a.S * kCluster), kWarps * 32, smem, 1, s, a)
+             : launch_dependent(balance_part_kernel<T, LPR, J, V, U>, dim3(a.chunks), kWarps * 32, smem, 1, s, a);
 }
 // vec: rows and pitches of whole groups of four logits
 template <class T>
@@ -689,17 +692,8 @@ int moe_balance_loss(int T, int E, int k, int S, const void* logits, long long l
                                                : launch_any<__nv_bfloat16>(a, vec, false, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   if (a.clusters && S == 1) return MOE_OK;
-  // a programmatic dependent: its blocks are placed while the first kernel ends (griddep_wait)
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = a.clusters ? dim3(1) : dim3(S, (E + 7) / 8);
-  cfg.blockDim = dim3(kJoin * 8);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, a.clusters ? balance_total_kernel : balance_join_kernel, a);
+  e = launch_dependent(a.clusters ? balance_total_kernel : balance_join_kernel, a.clusters ? dim3(1) : dim3(S, (E + 7) / 8),
+                       kJoin * 8, 0, 1, s, a);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

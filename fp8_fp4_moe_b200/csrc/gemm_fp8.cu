@@ -446,7 +446,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int rank = (int)cluster_ctarank();
   const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
 
-  if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);          // rank 0's producer; the bytes of both CTAs
@@ -471,6 +470,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tmem_relinquish_pair();
     tc_fence_before();
   }
+  griddep_wait();                      // nothing above touches global memory
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   __syncthreads();
   cluster_sync();                      // the peer's barriers are initialised before any remote use
   tc_fence_after();
@@ -741,7 +743,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
 
-  if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
@@ -766,6 +767,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
+  griddep_wait();                      // nothing above touches global memory
+  griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -1062,18 +1066,7 @@ cudaError_t launch(const Launch& l, int device, const CUtensorMap& tp, const CUt
       if (device < kMaxDevices) g_ready[device][l.slot] = true;
     }
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(l.threads);
-  cfg.dynamicSmemBytes = l.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.splits > 1 ? 1 : 0;     // the pair kernel carries its own
-  return cudaLaunchKernelEx(&cfg, l.fn, tp, tq, a);
+  return launch_dependent(l.fn, dim3(grid), l.threads, l.smem, a.splits, s, tp, tq, a);   // the pair kernel has its own pairs
 }
 
 // How a product is cut into tiles.

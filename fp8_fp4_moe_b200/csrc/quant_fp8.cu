@@ -267,6 +267,8 @@ __device__ __forceinline__ void column_amax(const Vec8<T> (&v)[8], float (&a)[8]
 // single row of activations already spreads over many SMs.  64 x 7168 bf16: 1.8 us, the time of a launch.
 template <class T, bool E5>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int kb = (p.K + 127) / 128;
   const long blocks = (long)p.M * kb;
   const int l16 = threadIdx.x & 15;
@@ -300,6 +302,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 3 : 4) quant_tile_kernel
   __shared__ __align__(16) uint8_t tr[128 * 128];   // transposed codes, 8-byte pieces XOR-swizzled
   __shared__ __align__(16) float cmax[8][128];      // of each warp's 16 rows
   __shared__ int cexp[128];
+  griddep_wait();
+  griddep_launch_dependents();
   const int tid = threadIdx.x, g = tid >> 4, c = tid & 15, lane = tid & 31;
   const int k0 = blockIdx.x * 128, m0 = blockIdx.y * 128;
   const int kc = k0 + c * 8;
@@ -395,13 +399,10 @@ cudaError_t launch_quant(const QuantArgs& a, bool tile, cudaStream_t s, int sms)
   if (!tile && a.qt == nullptr) {
     const long blocks = (long)a.M * kb, need = (blocks + 15) / 16;
     const int grid = (int)(need < 16l * sms ? need : 16l * sms);
-    quant_rows_kernel<T, E5><<<grid, 256, 0, s>>>(a);
-  } else if (tile) {
-    quant_tile_kernel<T, E5, true><<<dim3(kb, mb), 256, 0, s>>>(a);
-  } else {
-    quant_tile_kernel<T, E5, false><<<dim3(kb, mb), 256, 0, s>>>(a);
+    return launch_dependent(quant_rows_kernel<T, E5>, dim3(grid), 256, 0, 1, s, a);
   }
-  return cudaGetLastError();
+  return launch_dependent(tile ? quant_tile_kernel<T, E5, true> : quant_tile_kernel<T, E5, false>, dim3(kb, mb), 256, 0, 1,
+                          s, a);
 }
 
 template <class T>
