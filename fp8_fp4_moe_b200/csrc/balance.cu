@@ -3,7 +3,7 @@
 // Tokens t of sequence s (n_s of them count), scores p[t] = softmax(l[t]) or sigma(l[t]) / sum sigma(l[t]):
 //   c[s,e] = number of choices of expert e,  P[s,e] = (1 / n_s) sum_t p[t,e],
 //   L = coef / S' * sum_s E / (k n_s) * sum_e c[s,e] P[s,e],          S' = sequences with n_s > 0,
-//   dL/dl[t,e] = w_s / n_s * p[t,e] * (c[s,e] - sum_j c[s,j] p[t,j])  [ * (1 - sigma(l[t,e])) ],
+//   dL/dl[t,e] = w_s / n_s * p[t,e] * (c[s,e] - sum_j c[s,j] p[t,j])  [ * (1 - sigma(l[t,e])) ]  (p sums to 1),
 //   w_s = coef / S' * E / (k n_s).
 // The loss reads the logits once; the gradient needs the counts of all tokens, so it reads them again.
 // Sums over tokens run in a fixed order (per warp, per block, then over blocks), so results repeat bit
@@ -504,11 +504,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
       if (u > 0 && r0 + u * step >= p.T) break;            // the whole warp
       if (seq[u] >= 0 && seq[u] != have) {
         have = seq[u];
+        // counts as differences from the first one: the scores sum to 1, so a constant changes nothing, and what
+        // is subtracted below stays small (equal counts: exactly zero)
         const int32_t* cs = p.counts + (long)have * p.E;
+        const int c_ref = __ldg(cs);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int e = Map::expert(lane, j);
-          c[j] = e < p.E ? (float)__ldg(cs + e) : 0.f;
+          c[j] = e < p.E ? (float)(__ldg(cs + e) - c_ref) : 0.f;
         }
         const float n = (float)max(1, p.tokens[have]);
         g = grad_loss * p.coef * (float)p.E / ((float)p.k * (float)live) / n / n;

@@ -217,10 +217,17 @@ __device__ __forceinline__ void tile_coord(const Fp8Args& p, int tile, int& tp, 
   tp = band * kBand + (rem - tq * h);
 }
 
+// One addition per element and call, so their order is fixed; as a reduction it does not wait for the old value.
+__device__ __forceinline__ void add_to(float* p, float v) {
+  asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
 __device__ __forceinline__ void put_out(const Fp8Args& p, long m, long n, float v) {
   if (p.out_fp32) {
     float* o = static_cast<float*>(p.out) + m * p.ldo + n;
-    *o = p.accumulate ? *o + v : v;
+    if (p.accumulate)
+      add_to(o, v);
+    else
+      *o = v;
   } else {
     static_cast<__nv_bfloat16*>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
   }
@@ -261,7 +268,7 @@ __device__ __forceinline__ void flush_64b(const Fp8Args& p, uint8_t* buf, long r
       const uint4 w = *reinterpret_cast<const uint4*>(piece_at(buf, r, c));
       if (r < rows) {
         uint8_t* d = dst + (long)r * p.ldo * esize + c * 16;
-        if (p.accumulate)            // one addition per element and call: the order of them is fixed
+        if (p.accumulate)
           asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(d), "f"(__uint_as_float(w.x)),
                        "f"(__uint_as_float(w.y)), "f"(__uint_as_float(w.z)), "f"(__uint_as_float(w.w))
                        : "memory");
@@ -270,15 +277,20 @@ __device__ __forceinline__ void flush_64b(const Fp8Args& p, uint8_t* buf, long r
       }
     }
   } else {
+    const int shift = p.out_fp32 ? 4 : 5;
+#pragma unroll 8
     for (int i = lane; i < 32 * n; i += 32) {
-      const int r = i / n, c = i - r * n, byte = c * esize;
+      const int r = i >> shift, c = i & (n - 1), byte = c * esize;
       const uint8_t* at = piece_at(buf, r, byte >> 4) + (byte & 15);
       if (r < rows && c < cols) {
         const long o = (row0 + r) * p.ldo + col0 + c;
         if (p.out_fp32) {
           float* d = static_cast<float*>(p.out) + o;
           const float x = *reinterpret_cast<const float*>(at);
-          *d = p.accumulate ? *d + x : x;
+          if (p.accumulate)
+            add_to(d, x);
+          else
+            *d = x;
         } else {
           static_cast<uint16_t*>(p.out)[o] = *reinterpret_cast<const uint16_t*>(at);
         }

@@ -96,6 +96,16 @@ def test_extreme_logits(cuda_lib, score):
     assert (grad[0] == 0).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_equal_counts_have_no_gradient(cuda_lib, score):
+    # every token takes every expert: the loss is coef whatever the scores
+    l, _ = _inputs(11, 50, 8, 8)
+    ids = torch.arange(8, dtype=torch.int32).expand(50, 8).contiguous()
+    loss, counts, probs, tokens = binding.balance_loss(l.cuda(), ids.cuda(), coef=0.5, score=score)
+    grad = binding.balance_loss_backward(torch.ones((), device="cuda"), l.cuda(), counts, tokens, 8, coef=0.5, score=score)
+    assert (grad == 0).all() and abs(loss.item() - 0.5) <= 0.5 * (50 + 114) * U
+
+
 def test_what_a_mask_hides_is_not_read(cuda_lib):
     l, ids = _inputs(6, 100, 64, 3)
     mask = torch.ones(100, dtype=torch.bool)
