@@ -93,20 +93,20 @@ struct RowMap {
     for (int j = 0; j < J; j += V) {
       const int e = expert(lane, j);
       if constexpr (V == 4 && sizeof(T) == 4) {
-        const float4 v = live && e < E ? __ldg(reinterpret_cast<const float4*>(row + e))
+        const float4 v = live && e < E ? *reinterpret_cast<const float4*>(row + e)
                                        : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         l[j] = v.x;
         l[j + 1] = v.y;
         l[j + 2] = v.z;
         l[j + 3] = v.w;
       } else if constexpr (V == 4) {
-        const uint2 v = live && e < E ? __ldg(reinterpret_cast<const uint2*>(row + e)) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
+        const uint2 v = live && e < E ? *reinterpret_cast<const uint2*>(row + e) : make_uint2(0xFF80FF80u, 0xFF80FF80u);
         l[j] = __uint_as_float(v.x << 16);
         l[j + 1] = __uint_as_float(v.x & 0xFFFF0000u);
         l[j + 2] = __uint_as_float(v.y << 16);
         l[j + 3] = __uint_as_float(v.y & 0xFFFF0000u);
       } else if constexpr (sizeof(T) == 4) {
-        l[j] = live && e < E ? __ldg(row + e) : -INFINITY;
+        l[j] = live && e < E ? row[e] : -INFINITY;
       } else {
         l[j] = live && e < E ? __bfloat162float(row[e]) : -INFINITY;
       }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Starts start = stage_starts(p, starts_s);
-  const float grad_loss = __ldg(p.grad_loss);
+  const float grad_loss = *p.grad_loss;
   int live = 1;                        // sequences with tokens that count
   if (p.offsets != nullptr) {
     int alive = 0;
@@ -507,11 +507,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
         // counts as differences from the first one: the scores sum to 1, so a constant changes nothing, and what
         // is subtracted below stays small (equal counts: exactly zero)
         const int32_t* cs = p.counts + (long)have * p.E;
-        const int c_ref = __ldg(cs);
+        const int c_ref = cs[0];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int e = Map::expert(lane, j);
-          c[j] = e < p.E ? (float)(__ldg(cs + e) - c_ref) : 0.f;
+          c[j] = e < p.E ? (float)(cs[e] - c_ref) : 0.f;
         }
         const float n = (float)max(1, p.tokens[have]);
         g = grad_loss * p.coef * (float)p.E / ((float)p.k * (float)live) / n / n;

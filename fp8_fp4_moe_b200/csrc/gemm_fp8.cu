@@ -391,9 +391,9 @@ struct ScaleLoader {
       const long blk = is_p(i) ? p.sp_blk : p.sq_blk;
       if (quads && quad[is_p(i) ? 0 : 1]) {
         if constexpr (MX) {
-          v[i][0] = on ? __ldg(reinterpret_cast<const uint32_t*>(at[i])) : 0x7F7F7F7Fu;
+          v[i][0] = on ? *reinterpret_cast<const uint32_t*>(at[i]) : 0x7F7F7F7Fu;
         } else {
-          const uint4 w = on ? __ldg(reinterpret_cast<const uint4*>(at[i])) : make_uint4(0, 0, 0, 0);
+          const uint4 w = on ? *reinterpret_cast<const uint4*>(at[i]) : make_uint4(0, 0, 0, 0);
           v[i][0] = w.x;
           v[i][1] = w.y;
           v[i][2] = w.z;
@@ -401,7 +401,7 @@ struct ScaleLoader {
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = on && j < n ? __ldg(at[i] + j * blk) : kNone;
+        for (int j = 0; j < 4; ++j) v[i][j] = on && j < n ? at[i][j * blk] : kNone;
       }
       if (on) at[i] += 4 * blk;
     }
@@ -477,15 +477,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
   }
+  griddep_wait();                      // nothing above touches global memory
+  // TMEM only now: a block that held some while it waits for a kernel that has not allocated its own yet would
+  // keep that kernel from ending, on an SM that has room for both
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
     tc_fence_before();
   }
-  griddep_wait();                      // nothing above touches global memory
-  griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   __syncthreads();
+  griddep_launch_dependents();         // after the allocation, for the same reason
   cluster_sync();                      // the peer's barriers are initialised before any remote use
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -774,15 +776,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
   }
-  if (warp == 1) {
+  griddep_wait();                      // nothing above touches global memory
+  if (warp == 1) {                     // TMEM after the wait, the trigger after both, as in the pair kernel
     tmem_alloc(tmem_slot, C::kTmem);
     tmem_relinquish();
     tc_fence_before();
   }
-  griddep_wait();                      // nothing above touches global memory
-  griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;   // long before any wait can expire
   __syncthreads();
+  griddep_launch_dependents();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 

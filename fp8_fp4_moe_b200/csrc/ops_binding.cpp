@@ -118,10 +118,10 @@ PyObject* tuple(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
-template <PyObject* (*F)(PyObject* const*)>
+template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
-    (void)n;                                   // the Python side passes them all
+    if (n != N) type_error("takes ", N, " arguments, got ", n);
     return F(args);
   } catch (const Refused& e) {
     if (e.type) PyErr_SetString(e.type, e.what.c_str());
@@ -369,9 +369,9 @@ PyObject* balance_loss_backward(PyObject* const* a) {
   return wrap(out);
 }
 
-#define MOE_METHOD(name) {#name, (PyCFunction)(void (*)(void))entry<name>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {MOE_METHOD(quant_fp8), MOE_METHOD(gemm_fp8), MOE_METHOD(balance_loss),
-                         MOE_METHOD(balance_loss_backward), {nullptr, nullptr, 0, nullptr}};
+#define MOE_METHOD(name, n) {#name, (PyCFunction)(void (*)(void))entry<name, n>, METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {MOE_METHOD(quant_fp8, 10), MOE_METHOD(gemm_fp8, 8), MOE_METHOD(balance_loss, 7),
+                         MOE_METHOD(balance_loss_backward, 11), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -65,7 +65,7 @@ struct Vec8 {
     if (vec && n >= 8) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;
