@@ -504,15 +504,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
       if (u > 0 && r0 + u * step >= p.T) break;            // the whole warp
       if (seq[u] >= 0 && seq[u] != have) {
         have = seq[u];
-        // counts as differences from the first one: the scores sum to 1, so a constant changes nothing, and what
-        // is subtracted below stays small (equal counts: exactly zero)
+        // counts above the least one: the scores sum to 1, so a constant changes nothing, and what is subtracted
+        // below is no larger than the counts themselves (equal counts: exactly zero)
         const int32_t* cs = p.counts + (long)have * p.E;
-        const int c_ref = cs[0];
+        const uint32_t row_lanes = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1) << (lane & ~(LPR - 1));
+        int least = INT32_MAX;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int e = Map::expert(lane, j);
-          c[j] = e < p.E ? (float)(cs[e] - c_ref) : 0.f;
+          const int v = e < p.E ? cs[e] : INT32_MAX;
+          c[j] = __int_as_float(v);
+          least = min(least, v);
         }
+        least = __reduce_min_sync(row_lanes, least);   // the row's lanes are here together
+#pragma unroll
+        for (int j = 0; j < J; ++j) c[j] = Map::expert(lane, j) < p.E ? (float)(__float_as_int(c[j]) - least) : 0.f;
         const float n = (float)max(1, p.tokens[have]);
         g = grad_loss * p.coef * (float)p.E / ((float)p.k * (float)live) / n / n;
       }

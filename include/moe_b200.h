@@ -416,10 +416,11 @@ int moe_gemm_fp8(int M, int N, int K, const void* A, long long lda, int a_format
  * logits [T][E] fp32 or bf16, row pitch ldl; topk_ids int32 [T][k], entries outside [0, E) are not
  * counted; offsets int32 [S + 1] ascending: sequence s is tokens [offsets[s], offsets[s + 1]), tokens
  * outside all of them do not count; NULL (then S = 1) = all T tokens; mask uint8 [T], 0 = the token does
- * not count (its logits are not read); NULL = all count.  A logit of -inf gives a score of 0, a row of
- * them scores of 0 throughout; NaN and +inf give NaN.  Outputs: loss fp32 [1], counts int32 [S][E], probs
- * fp32 [S][E], tokens int32 [S] (n_s).  Sums run in fp32 in a fixed order (the loss in fp64): results
- * repeat bit for bit.  Shapes: 0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 2^20.
+ * not count (its logits are not read); NULL = all count.  A logit of -inf gives a score of 0, a row of them
+ * scores of 0 throughout; NaN gives NaN, and so does +inf in a softmax (its sigmoid is 1).  Outputs: loss fp32
+ * [1], counts int32 [S][E], probs fp32 [S][E], tokens int32 [S] (n_s).  Sums run in fp32 in a fixed order (the
+ * loss in fp64): results repeat bit for bit.  Shapes: 0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 16), 1
+ * <= S <= 2^20.
  * Workspace: 256-byte aligned, moe_balance_workspace_bytes(T, E, S) (0 for an unsupported shape); calls
  * that may overlap on the device need their own.  Asynchronous on `stream`. */
 enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };

@@ -106,6 +106,37 @@ def test_equal_counts_have_no_gradient(cuda_lib, score):
     assert (grad == 0).all() and abs(loss.item() - 0.5) <= 0.5 * (50 + 114) * U
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 64, 600])
+def test_gradient_beside_a_popular_expert_of_low_score(cuda_lib, score, E):
+    # all choose expert 0, whose score is small: the others' gradient, p (0 - mean) with a mean near 0, keeps its digits
+    l, _ = _inputs(12, 300, E, 1)
+    l[:, 0] -= 20
+    _check(l, torch.zeros(300, 1, dtype=torch.int32), score=score)
+    off = torch.tensor([0, 7, 7, 130, 301 - 1], dtype=torch.int32)
+    _check(l, torch.zeros(300, 1, dtype=torch.int32), offsets=off, score=score)
+
+
+def test_infinite_logits(cuda_lib):
+    # sigmoid(inf) is 1; a softmax with an infinity is undefined, in its row alone
+    l, ids = _inputs(13, 30, 16, 2)
+    l[4, 5] = float("inf")
+    args = dict(coef=0.01, score="sigmoid")
+    loss, counts, probs, tokens = binding.balance_loss(l.cuda(), ids.cuda(), **args)
+    grad = binding.balance_loss_backward(torch.ones((), device="cuda"), l.cuda(), counts, tokens, 2, **args)
+    v, n = l.double().numpy(), ids.numpy()
+    p = O.scores(v, "sigmoid")
+    c = O.balance_loss(v, n, 0.01, score="sigmoid")[1]
+    whole = 0.01 * 16 / 2 / 30 / 30 * p * (c + (p * c).sum(1, keepdims=True))   # the magnitudes without 1 - sigma
+    ref, mag = O.balance_grad(1.0, v, n, 0.01, score="sigmoid")
+    assert ref[4, 5] == 0 and (np.abs(grad.cpu().numpy() - ref) <= U * (300 * mag + 8 * whole)).all()
+    assert abs(loss.item() - O.balance_loss(v, n, 0.01, score="sigmoid")[0]) <= (30 + 116) * U * loss.item()
+    loss, counts, probs, tokens = binding.balance_loss(l.cuda(), ids.cuda())
+    grad = binding.balance_loss_backward(torch.ones((), device="cuda"), l.cuda(), counts, tokens, 2)
+    assert torch.isnan(loss) and torch.isnan(grad[4]).any()
+    assert torch.isfinite(grad[:4]).all() and torch.isfinite(grad[5:]).all()
+
+
 def test_what_a_mask_hides_is_not_read(cuda_lib):
     l, ids = _inputs(6, 100, 64, 3)
     mask = torch.ones(100, dtype=torch.bool)
@@ -194,3 +225,21 @@ def test_offsets_that_do_not_ascend_stay_in_bounds(cuda_lib):
     binding.balance_loss_backward(torch.ones((), device="cuda"), l.cuda(), counts, tokens, 2, offsets=off, out=pad[1:65])
     torch.cuda.synchronize()
     assert (pad[0] == 7).all() and (pad[65] == 7).all()
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """More than 2^31 logits: the last sequence's results are those of its tokens alone."""
+    T, E, k, tail = (1 << 23) + 77, 257, 2, 900
+    l = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+    l.uniform_(-3, 3)
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    one = torch.ones((), device="cuda")
+    loss, counts, probs, tokens = binding.balance_loss(l, ids, offsets=off)
+    grad = binding.balance_loss_backward(one, l, counts, tokens, k, offsets=off)
+    _, c, p, n, g = _check(l[-tail:].cpu(), ids[-tail:].cpu())
+    g = binding.balance_loss_backward(one, l[-tail:], c, n, k, coef=0.5)       # half the loss: one of two sequences
+    assert torch.equal(counts[1], c[0]) and tokens.tolist() == [T - tail, tail]
+    assert (probs[1] - p[0]).abs().max() <= 2 * (tail + 114) * U * p.max()
+    assert (grad[-tail:].float() - g.float()).abs().max() <= 2.0 ** -7 * g.float().abs().max()
+    assert int(counts[0].sum()) == (T - tail) * k
