@@ -281,3 +281,85 @@ def test_training_step_of_a_linear_layer(cuda_lib, T, H, N, scale_dtype):
     # (E4M3) or 2^-3 (E5M2) of the element (codes below the format's normal range: of amax 2^-15 at most)
     xd, wd = x.double().cpu().numpy(), w.double().cpu().numpy()
     assert (np.abs(y.double().cpu().numpy() - xd @ wd.T) <= (2 * 2.0 ** -4 + 2.0 ** -7) * 1.01 * (np.abs(xd) @ np.abs(wd).T) + 1e-2 * np.sqrt(H)).all()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "ue8m0"])
+def test_offsets_beyond_32_bits(cuda_lib, kind):
+    """An output of more than 2^31 elements, and operand rows more than 2^31 bytes apart."""
+    M, N, K = 66000, 32776, 130
+    st = torch.float32 if kind == "fp32" else torch.uint8
+    x = torch.randn(M, K, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(N, K, device="cuda", dtype=torch.bfloat16)
+    A, As, _, _ = binding.quant_fp8(x, scale_dtype=st)
+    B, Bs, _, _ = binding.quant_fp8(w, block="tile", scale_dtype=st)
+    out, _ = binding.gemm_fp8(A, As, B, Bs)
+    tail, _ = binding.gemm_fp8(A[-200:], As[-200:], B, Bs)
+    assert torch.equal(out[-200:], tail)
+    head, _ = binding.gemm_fp8(A[:200], As[:200], B, Bs)
+    assert torch.equal(out[:200], head)
+    del out
+    wide = torch.empty(M, 32784, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[:, 16:16 + K]
+    wide.copy_(A)
+    narrow = B[:300]
+    Bs300 = Bs[:3]
+    a, _ = binding.gemm_fp8(wide, As, narrow, Bs300)
+    b, _ = binding.gemm_fp8(A, As, narrow, Bs300)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "ue8m0"])
+def test_product_with_itself(cuda_lib, kind):
+    rng = np.random.default_rng(40)
+    a, A = _codes(rng, 300, 400, "e4m3")
+    s, As = _scales(rng, 300, 400, "row", kind)
+    out, ws = binding.gemm_fp8(A, As, A, As, out_dtype=torch.float32)
+    _equal(out, ws, O.gemm(a, s, a, s)[0])
+
+
+@pytest.mark.parametrize("scale_dtype", [torch.float32, torch.uint8])
+@pytest.mark.parametrize("M", [1, 100, 700])
+def test_captured_layer_step_follows_its_inputs(cuda_lib, M, scale_dtype):
+    """Copies, memsets, two branches that join, and calls that follow one another without a gap, as one graph: replayed on
+    new inputs it gives what the calls give one by one."""
+    N, K = 520, 384
+    src = torch.empty(M, K, device="cuda", dtype=torch.bfloat16)
+    src2 = torch.empty(N, K, device="cuda", dtype=torch.bfloat16)
+    x, w = torch.empty_like(src), torch.empty_like(src2)
+    acc = torch.empty(M, N, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        x.copy_(src)
+        acc.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            w.copy_(src2)
+            B, Bs, _, _ = binding.quant_fp8(w, block="tile", scale_dtype=scale_dtype)
+        A, As, _, _ = binding.quant_fp8(x, scale_dtype=scale_dtype)
+        main.wait_stream(side)
+        y, ws = binding.gemm_fp8(A, As, B, Bs)
+        binding.gemm_fp8(A, As, B, Bs, out=acc, accumulate=True, workspace=ws)
+        binding.gemm_fp8(A, As, B, Bs, out=acc, accumulate=True, workspace=ws)
+        q, s, _, _ = binding.quant_fp8(y, scale_dtype=scale_dtype)
+        z, _ = binding.gemm_fp8(q, s, q, s, workspace=ws, out_dtype=torch.float32)
+        return y, acc.clone(), z, ws
+
+    src.normal_(), src2.normal_()
+    torch.cuda.synchronize()
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for _ in range(5):
+        src.normal_(), src2.normal_()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        have = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(have[:3], want[:3]):
+            assert torch.equal(a, b)
+        assert have[3][:16].view(torch.int32)[0].item() == 0

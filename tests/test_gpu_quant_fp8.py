@@ -159,3 +159,20 @@ def test_other_stream_and_graph(cuda_lib):
     want = binding.quant_fp8(buf, cols=True)
     for a, b in zip(want, got):
         assert torch.equal(a.float(), b.float())
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+def test_offsets_beyond_32_bits(cuda_lib, block):
+    """More than 2^31 elements: the last rows, and the last columns of the transposed copy, are those of the rows alone."""
+    M, K, tail = 66048, 32776, 384                        # tail starts a row block of the transposed copy
+    x = torch.empty(M, K, device="cuda", dtype=torch.bfloat16)
+    x.normal_()
+    q, s, qt, st = binding.quant_fp8(x, block=block, rows=True, cols=True)
+    want = binding.quant_fp8(x[-tail:], block=block, rows=True, cols=True)
+    n = tail if block == "row" else tail // 128
+    assert torch.equal(q[-tail:].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s[-n:], want[1])
+    assert torch.equal(qt[:, -tail:].view(torch.uint8), want[2].view(torch.uint8)) and torch.equal(st[:, -3:], want[3])
+    del qt, st
+    if block == "row":
+        only, so, _, _ = binding.quant_fp8(x)
+        assert torch.equal(only.view(torch.uint8), q.view(torch.uint8)) and torch.equal(so, s)
