@@ -508,17 +508,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
         // below is no larger than the counts themselves (equal counts: exactly zero)
         const int32_t* cs = p.counts + (long)have * p.E;
         const uint32_t row_lanes = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1) << (lane & ~(LPR - 1));
-        int least = INT32_MAX;
+        int least = INT32_MAX;           // of a first reading: kept, the counts would not fit the registers
+#pragma unroll 16
+        for (int e = lane % LPR; e < p.E; e += LPR) least = min(least, cs[e]);
+        least = __reduce_min_sync(row_lanes, least);       // the row's lanes are here together
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int e = Map::expert(lane, j);
-          const int v = e < p.E ? cs[e] : INT32_MAX;
-          c[j] = __int_as_float(v);
-          least = min(least, v);
+          c[j] = e < p.E ? (float)(cs[e] - least) : 0.f;
         }
-        least = __reduce_min_sync(row_lanes, least);   // the row's lanes are here together
-#pragma unroll
-        for (int j = 0; j < J; ++j) c[j] = Map::expert(lane, j) < p.E ? (float)(__float_as_int(c[j]) - least) : 0.f;
         const float n = (float)max(1, p.tokens[have]);
         g = grad_loss * p.coef * (float)p.E / ((float)p.k * (float)live) / n / n;
       }
