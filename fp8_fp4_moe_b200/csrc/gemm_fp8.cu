@@ -155,6 +155,13 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+// ... x 16 columns: r[0..7]
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
@@ -436,11 +443,12 @@ __device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int j) { return id
 // What bounds it (8192 x 4096 x 7168, 481 GFLOP): UE8M0 170 us, 2.8 PFLOP/s -- the power limit, under which the SM clock
 // falls to about 1.4 GHz, and the last wave of tiles; tensor pipe busy three quarters of the cycles at 2048 rows.
 // fp32 scales 228 us, 2.1 PFLOP/s: the epilogue warps' TMEM reads and one FMA per element and K block beside the
-// MMAs.  QROW 362 us at 4096 x 7168 x 8192, 1.3 PFLOP/s: a second fp32 operation per element and the column
+// MMAs.  QROW 350 us at 4096 x 7168 x 8191, 1.4 PFLOP/s: a second fp32 operation per element and the column
 // scales' shared-memory reads.
 // QROW (fp32 scales only): Q's scales differ by column; otherwise one per 128 columns, and every tile
 // starts at a multiple of 128.  NC: columns of an epilogue thread; with fp32 scales bn = 2 NC, known to the
-// compiler so that it can move loads and additions of different columns past each other; UE8M0: up to NC.
+// compiler so that it can move loads and additions of different columns past each other (NC = 112: the
+// last 16 of them by themselves); UE8M0: up to NC.
 template <bool MX, bool QROW, int NC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
@@ -503,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   // scales: as many as fit, up to four: from the end of a block's MMAs to the next use of its buffer lie about
   // 900 clocks of commits, waits and the arrival at the other CTA, which only other buffers' MMAs fill
   const int na = MX ? (bn > 224 ? 1 : 2) : min(4, 512 / bn);
-  const uint32_t acc_cols = MX ? 256 : bn;
+  const uint32_t acc_cols = MX || bn > 128 ? 256 : bn;
   const uint32_t sf_col = bn > 224 ? 256 : 224;
 
   // fp32 scales: the epilogue warps hold 128 accumulators each, beyond the 168 registers a thread of 12
@@ -608,7 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
       };
-      constexpr int kHalf = (4 + NC / 16) / 2;   // QROW: the items of two warps, which have 72 registers
+      constexpr int kItems = 4 + NC / 16, kHalf = (kItems + 1) / 2;   // QROW: the items of two warps, which have 72 registers
       if (warp == 2) {
         if constexpr (MX)
           feed(ScaleLoader<true, 0, 12, true>());
@@ -617,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         else
           feed(ScaleLoader<false, 0, 5, false>());
       } else if constexpr (!MX && QROW) {
-        feed(ScaleLoader<false, kHalf, kHalf, true>());
+        feed(ScaleLoader<false, kHalf, kItems - kHalf, true>());
       }
     }
   } else {
@@ -625,8 +633,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------------------ epilogue (warps 4..11, both CTAs)
     const int q = warp & 3, half = (warp - 4) >> 2;
     uint8_t* obuf = smem + C::staging + (warp - 4) * 2048;
-    // columns [0, h) and [h, bn), h a multiple of 32; both kinds of warp sit on every scheduler
-    const int h = (bn / 2 + 31) & ~31, c0 = half ? h : 0, nc = MX ? (half ? bn - h : h) : NC;
+    // columns [0, h) and [h, bn), UE8M0: h a multiple of 32; both kinds of warp sit on every scheduler
+    const int h = MX ? (bn / 2 + 31) & ~31 : NC, c0 = half ? h : 0, nc = half ? bn - h : h;
     const uint32_t t_acc = tmem + c0 + ((uint32_t)(q * 32) << 16), acce0 = mapa_shared(acce, 0);
     int buf = 0, slot = 0;
     uint32_t aphase = 0, rphase = 0;
@@ -634,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (int tile = first; tile < tiles; tile += step) {
       int tp, tq;
       tile_coord(p, tile, tp, tq);
-      float acc[NC];
+      float acc[(NC + 31) / 32 * 32];
       if constexpr (MX) {
         ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue));
         if (!ok) break;
@@ -649,13 +657,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (++buf == na) { buf = 0; aphase ^= 1; }
       } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) acc[c] = 0.f;
+        for (int c = 0; c < (NC + 31) / 32 * 32; ++c) acc[c] = 0.f;
         // 32 columns at a time, the next ones on their way from TMEM while these are added
         auto load = [&](int c, uint32_t* r) {
           const uint32_t t = t_acc + buf * acc_cols + c;
           if constexpr (QROW) {
-            tmem_ld_frag(t, r);
-            tmem_ld_frag(t + (16u << 16), r + 16);
+            if (c + 32 <= NC) {
+              tmem_ld_frag(t, r);
+              tmem_ld_frag(t + (16u << 16), r + 16);
+            } else {
+              tmem_ld_frag16(t, r);
+              tmem_ld_frag16(t + (16u << 16), r + 16);
+            }
           } else {
             tmem_ld<32>(t, r);
           }
@@ -679,8 +692,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           load(0, r[0]);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < NC / 32; ++i) {
-            if (i + 1 < NC / 32) {
+          for (int i = 0; i < (NC + 31) / 32; ++i) {
+            if (i + 1 < (NC + 31) / 32) {
               load((i + 1) * 32, r[(i + 1) & 1]);
             } else {                             // everything is read: the buffer may be overwritten
               tc_fence_before();
@@ -693,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               // 8 bytes of column scales serve four rows: with a row to a lane, every lane would read all
               // columns' scales, and shared memory returns 128 bytes a clock whether they differ or not
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < (i * 32 + 32 <= NC ? 4 : 2); ++j) {
                 const float2 sq = *reinterpret_cast<const float2*>(sc + BM + c0 + i * 32 + 8 * j + 2 * (lane & 3));
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -706,7 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) a[j] = fmaf(__uint_as_float(v[j]), sp[0], a[j]);
             }
-            if (i + 1 < NC / 32) tmem_ld_wait();
+            if (i + 1 < (NC + 31) / 32) tmem_ld_wait();
           }
           if (++buf == na) { buf = 0; aphase ^= 1; }
           if (j4 == 3 || kb == KB - 1) {
@@ -1052,6 +1065,7 @@ Launch pair_of(bool mx, bool qrow, int bn) {
   if (bn == 256)
     return qrow ? Launch{gemm_fp8_pair_kernel<false, true, 128>, PairCfg<false>::bytes, kPairThreads, 9}
                 : Launch{gemm_fp8_pair_kernel<false, false, 128>, PairCfg<false>::bytes, kPairThreads, 10};
+  if (bn == 224) return {gemm_fp8_pair_kernel<false, true, 112>, PairCfg<false>::bytes, kPairThreads, 13};
   return qrow ? Launch{gemm_fp8_pair_kernel<false, true, 64>, PairCfg<false>::bytes, kPairThreads, 11}
               : Launch{gemm_fp8_pair_kernel<false, false, 64>, PairCfg<false>::bytes, kPairThreads, 12};
 }
@@ -1060,7 +1074,7 @@ Launch pair_of(bool mx, bool qrow, int bn) {
 constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
 int g_sms[kMaxDevices] = {};
-bool g_ready[kMaxDevices][13] = {};
+bool g_ready[kMaxDevices][14] = {};
 
 int device_sms(int* device) {
   int dev = -1;
@@ -1130,7 +1144,9 @@ Cut choose(int M, int N, int KB, int sms, bool qrow, bool mx) {
   }
   if (!swap)
     for (int bn = 256; bn >= 64; bn -= 32) {
-      if (!mx && bn != 256 && bn != 128) continue;                 // the widths compiled for fp32 scales
+      // the widths compiled for fp32 scales.  224, column scales: 4096 x 7168 x 8191 is 512 tiles, 6.9 waves, 350 us; with
+      // 256 columns 448 tiles in 6.05 waves, 366 us.  Scales per 128 columns need tiles that start with them
+      if (!mx && bn != 256 && bn != 128 && !(qrow && bn == 224)) continue;
       const double waves = (double)up((long)up(M, 256) * up(N, bn), sms / 2);
       const double block = mx ? 0.130 + 0.00124 * bn : qrow ? 0.231 + 0.0023 * bn : 0.131 + 0.00172 * bn;
       offer(Cut{true, false, bn, 1}, waves * KB, block, 2.0 + 0.3 * waves);

@@ -363,3 +363,16 @@ def test_captured_layer_step_follows_its_inputs(cuda_lib, M, scale_dtype):
         for a, b in zip(have[:3], want[:3]):
             assert torch.equal(a, b)
         assert have[3][:16].view(torch.int32)[0].item() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 5000, 2000), (520, 7001, 1300), (300, 5888, 2048)])
+@pytest.mark.parametrize("b_per", ["row", "tile"])
+def test_exact_pair_tiles_of_224_columns(cuda_lib, M, N, K, b_per):
+    """One wave of CTA pairs (column scales: 224 columns, 112 to each half).  Sums stay below 25 * 64 * 2048 = 3.3e6 <
+    2^24 units, also with 7000 added."""
+    ref, A, As, B, Bs = _case(50, M, N, K, "fp32", b_per=b_per)
+    out, ws = binding.gemm_fp8(A, As, B, Bs)
+    _equal(out, ws, ref)
+    acc = torch.full((M, N), 7000.0, device="cuda")
+    binding.gemm_fp8(A, As, B, Bs, out=acc, accumulate=True, workspace=ws)
+    _equal(acc, ws, ref + 7000)
