@@ -252,6 +252,13 @@ __device__ __forceinline__ void put_out4(const Fp8Args& p, long m, long n, float
     return;
   }
   const float f[4] = {v.x, v.y, v.z, v.w};
+  if (p.out_fp32 && !p.accumulate) {   // one look at the kind of output for all four
+    float* o = static_cast<float*>(p.out) + m * p.ldo + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < n_end) o[i] = f[i];
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (n + i < n_end) put_out(p, m, n + i, f[i]);
