@@ -139,7 +139,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // exp(l - m) as 2^(l log2(e) - m log2(e)), one FMA: the rounding of m log2(e) is common to the row and cancels in the
-// quotient, that of the result is at most that of l - m.
+// quotient, that of the result is at most that of l - m.  It has to be small for that: up to |m| = 1e6 it is at most
+// 1/16 in the exponent, at 5e9 it takes every term to zero or infinity.  Rows above take the difference first.
+constexpr float kFusedLogit = 1e6f;
 template <int LPR, int J>
 __device__ __forceinline__ void softmax_row(float (&l)[J]) {
   float m = -INFINITY;
@@ -147,7 +149,7 @@ __device__ __forceinline__ void softmax_row(float (&l)[J]) {
   for (int j = 0; j < J; ++j) m = fmaxf(m, l[j]);
   m = row_max<LPR>(m);
   float z = 0.f;
-  if (__any_sync(0xffffffffu, fabsf(m) > 1e30f)) {   // m log2(e) may overflow, or nothing is finite
+  if (__any_sync(0xffffffffu, fabsf(m) > kFusedLogit)) {   // far from zero, or nothing is finite
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       l[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - m);
