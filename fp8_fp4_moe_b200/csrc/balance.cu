@@ -14,6 +14,7 @@
 // launches and their latencies.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -137,6 +138,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // exp(l - m) as 2^(l log2(e) - m log2(e)), one FMA: the rounding of m log2(e) is common to the row and cancels in the
 // quotient, that of the result is at most that of l - m.  It has to be small for that: up to |m| = 1e6 it is at most
@@ -169,30 +175,79 @@ __device__ __forceinline__ void softmax_row(float (&l)[J]) {
   for (int j = 0; j < J; ++j) l[j] *= r;
 }
 
-// l: a token's logits -> its scores; returns Z = sum of sigma(l) for sigmoid scores, so that sigma = l Z (0: they are
-// too small for that, and 1 - sigma is 1).  A row whose logits are all -inf has zero scores, and so has a token
-// that does not count (not live: its logits read as -inf).  All lanes of the warp call it.
+// Sigmoid scores from one exponential each: with s = min(largest logit of the row, 0), a = e^s and y = e^(s - l),
+//   w = 1 / (a + y) = sigma(l) e^-s,   p = w / sum w,   sigma = a w,   1 - sigma = y w.
+// Some w of a row is at least 1/2, however low its logits are, and 1 - sigma needs no difference where it is small.
+// l: logits -> y, returns a.  A row without a finite logit, and a token that does not count (its logits read
+// as -inf), have y = infinity throughout: zero scores.  All lanes of the warp call it.  Where every row has a logit
+// above zero, s is 0 without a reduction.
 template <int LPR, int J>
-__device__ __forceinline__ float scores(int score, bool live, float (&l)[J]) {
+__device__ __forceinline__ float sigmoid_row(float (&l)[J]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < J; ++j) m = fmaxf(m, l[j]);
+  const uint32_t above = __ballot_sync(0xffffffffu, m >= 0.f), row = LPR == 32 ? 0xffffffffu : (1u << LPR) - 1;
+  bool low = false;
+#pragma unroll
+  for (int i = 0; i < 32; i += LPR) low |= (above >> i & row) == 0;
+  float s = 0.f;
+  if (low) {                           // the whole warp
+    m = row_max<LPR>(m);
+    s = m == -INFINITY ? 0.f : fminf(m, 0.f);
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j) l[j] = ex2((s - l[j]) * kLog2e);
+  return ex2(s * kLog2e);
+}
+
+// l: a token's logits -> its scores.  A row whose logits are all -inf has zero scores, and so has a token that does
+// not count.  All lanes of the warp call it.
+template <int LPR, int J>
+__device__ __forceinline__ void scores(int score, float (&l)[J]) {
   if (score != MOE_SCORE_SIGMOID) {
     softmax_row<LPR, J>(l);
-    return 0.f;
+    return;
   }
+  const float a = sigmoid_row<LPR, J>(l);
   float z = 0.f;
 #pragma unroll
-  for (int j = 0; j < J; ++j) z += __fdividef(1.f, 1.f + ex2(-l[j] * kLog2e));
-  z = row_sum<LPR>(z);
-  const bool tiny = live && z < 1e-30f;
-  if (__any_sync(0xffffffffu, tiny)) { // every sigma of a row underflows: the warp's rows from their logarithms
-#pragma unroll
-    for (int j = 0; j < J; ++j) l[j] = fminf(l[j], 0.f) - log1pf(expf(-fabsf(l[j])));
-    softmax_row<LPR, J>(l);
-  } else {
-    const float r = live ? 1.f / z : 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) l[j] = __fdividef(1.f, 1.f + ex2(-l[j] * kLog2e)) * r;
+  for (int j = 0; j < J; ++j) {
+    l[j] = rcp(a + l[j]);
+    z += l[j];
   }
-  return tiny ? 0.f : z;
+  z = row_sum<LPR>(z);
+  const float r = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+  for (int j = 0; j < J; ++j) l[j] *= r;
+}
+
+// l: a token's logits -> its scores, with sigmoid scores times 1 - sigma; returns sum_j c_j p_j.
+template <int LPR, int J>
+__device__ __forceinline__ float weighted_scores(int score, const float (&c)[J], float (&l)[J]) {
+  float mean = 0.f;
+  if (score != MOE_SCORE_SIGMOID) {
+    softmax_row<LPR, J>(l);
+#pragma unroll
+    for (int j = 0; j < J; ++j) mean = fmaf(c[j], l[j], mean);
+    return row_sum<LPR>(mean);
+  }
+  const float a = sigmoid_row<LPR, J>(l);
+  float z = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float w = rcp(a + l[j]);
+    z += w;
+    mean = fmaf(c[j], w, mean);
+  }
+  z = row_sum<LPR>(z);
+  mean = row_sum<LPR>(mean);
+  const float r = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const float w = rcp(a + l[j]);
+    l[j] = fminf(l[j], FLT_MAX) * w * (w * r);             // (1 - sigma) p; w is 0 where y is infinite
+  }
+  return mean * r;
 }
 
 // Sums over tokens [a, b) by one block: sum_s[warp][E] of scores, cnt_s[E] of choices, n_s tokens that count.  The
@@ -234,7 +289,7 @@ __device__ __forceinline__ void sum_tokens(const BalanceArgs& p, int a, int b, f
     for (int u = 0; u < U; ++u) {
       n += live[u] && lane % LPR == 0;
       if (u == 0 || __any_sync(0xffffffffu, live[u])) {
-        scores<LPR, J>(p.score, live[u], l[u]);
+        scores<LPR, J>(p.score, l[u]);
 #pragma unroll
         for (int j = 0; j < J; ++j) acc[j] += l[u][j];
       }
@@ -526,11 +581,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
         const float n = (float)max(1, p.tokens[have]);
         g = grad_loss * p.coef * (float)p.E / ((float)p.k * (float)live) / n / n;
       }
-      const float z = scores<LPR, J>(p.score, seq[u] >= 0, l[u]);
-      float mean = 0.f;
-#pragma unroll
-      for (int j = 0; j < J; ++j) mean = fmaf(c[j], l[u][j], mean);
-      mean = row_sum<LPR>(mean);
+      const float mean = weighted_scores<LPR, J>(p.score, c, l[u]);
       const bool write = t < p.T && (seq[u] >= 0 || !p.accumulate);
       T* out = static_cast<T*>(p.grad) + (long)t * p.ldg;
 #pragma unroll
@@ -539,7 +590,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) balance_grad_kernel(const Bala
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           d[v] = g * l[u][j + v] * (c[j + v] - mean);
-          if (p.score == MOE_SCORE_SIGMOID) d[v] *= 1.f - l[u][j + v] * z;
           if (seq[u] < 0) d[v] = 0.f;
         }
         const int e = Map::expert(lane, j);
