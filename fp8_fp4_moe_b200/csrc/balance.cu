@@ -452,7 +452,9 @@ __global__ void __launch_bounds__(kTotal * 32) balance_total_kernel(const Balanc
   write_total(p, p.S);
 }
 
-// One block per (sequence, 8 experts): the slots of the sequence added up in order, every 32nd by one thread.
+// One block per (sequence, 8 experts): the slots of the sequence, any number of them, added up in order, every 32nd by
+// one thread.  Each addition's rounding is carried to the next one (Kahan), so that the number of slots does not count;
+// in 64 bits, and one after the other at the end, 1.4 us more at 293 slots.
 // The last block of the grid adds up the loss.
 constexpr int kJoin = 32;
 static_assert(kJoin * 8 == kTotal * 32, "the join kernel's last block writes the total");
@@ -468,15 +470,15 @@ __global__ void __launch_bounds__(kJoin * 8) balance_join_kernel(const BalanceAr
   const Starts start{p.offsets, p.S, p.T};
   const int a = start[s], b = start[s + 1];
   const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk + 1 : c0;   // chunks of the sequence
-  float vp = 0.f;
+  float vp = 0.f, lost = 0.f;
   int vc = 0, vn = 0;
 #pragma unroll 8
   for (int c = c0 + w; c < c1; c += kJoin) {
     const long slot = c + s;
-    if (e < p.E) {
-      vp += p.part_p[slot * p.E + e];
-      vc += p.part_c[slot * p.E + e];
-    }
+    const float x = (e < p.E ? p.part_p[slot * p.E + e] : 0.f) - lost, sum = vp + x;
+    vc += e < p.E ? p.part_c[slot * p.E + e] : 0;
+    lost = (sum - vp) - x;
+    vp = sum;
     vn += p.part_n[slot];
   }
   fp[w][x] = vp;
@@ -484,14 +486,19 @@ __global__ void __launch_bounds__(kJoin * 8) balance_join_kernel(const BalanceAr
   if (x == 0) fn[w] = vn;
   __syncthreads();
   if (threadIdx.x < 32) {              // lanes 8 and up repeat the first ones' experts
-    vp = 0.f;
+    float sums[kJoin];                 // in pairs, in pairs of pairs, ...
     vc = vn = 0;
 #pragma unroll
     for (int i = 0; i < kJoin; ++i) {
-      vp += fp[i][x];
+      sums[i] = fp[i][x];
       vc += fc[i][x];
       vn += fn[i];
     }
+#pragma unroll
+    for (int o = kJoin / 2; o >= 1; o /= 2)
+#pragma unroll
+      for (int i = 0; i < o; ++i) sums[i] += sums[i + o];
+    vp = sums[0];
     const float mean = vn > 0 ? vp / (float)vn : 0.f;
     if (w == 0 && e < p.E) {
       p.counts[(long)s * p.E + e] = vc;
@@ -640,11 +647,14 @@ struct Layout {
 };
 
 // About two blocks per SM (with four rows of 1 KB to a warp, 64 KB of logits in flight an SM), and a round of
-// all warps at least.
+// all warps at least.  At most 4096 tokens: a lane adds 128 scores of an expert then (E > 256: 256, E > 512: 512), and
+// additions of like scores all round the same way, so that a chain is off by up to its length times 2^-24.  A block of
+// 4096 tokens runs for about 100 us, beside which its start costs nothing.
+constexpr int kChunk = 4096;
 Layout layout(int T, int E, int S) {
   Layout L;
   const int chunk = ((T + 2 * 148 - 1) / (2 * 148) + 15) / 16 * 16;
-  L.chunk = chunk < 32 ? 32 : chunk;
+  L.chunk = chunk < 32 ? 32 : chunk > kChunk ? kChunk : chunk;
   L.chunks = (T + L.chunk - 1) / L.chunk;
   const size_t slots = (size_t)L.chunks + (size_t)S;
   L.part_p = 0;
