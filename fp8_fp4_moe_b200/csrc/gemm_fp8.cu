@@ -363,6 +363,33 @@ __device__ __forceinline__ void store_frags(const Fp8Args& p, uint8_t* buf, cons
   }
 }
 
+// fp32 scales may have any finite value.  Two of magnitudes in [2^-62, 2^63), or zero, have a product that is normal or
+// zero, and a block sum takes it in one FMA.  In a group of four K blocks with others (a byte per slot and scale
+// warp tells the epilogue) the two are applied one after the other where need be (add_scaled).  That loop holds its sums in
+// local memory and looks at few columns at a time, so that the ordinary one keeps its registers: with both additions in
+// one loop 8192 x 4096 x 7168 took 265 us, not 227, column scales 453 at 4096 x 7168 x 8191, not 336.
+__device__ __forceinline__ bool plain_scale(uint32_t bits) {
+  constexpr uint32_t lo = (127u - 62) << 23, hi = (127u + 63) << 23;
+  const uint32_t u = bits & 0x7FFFFFFFu;
+  return u - lo < hi - lo || u == 0;
+}
+__device__ __forceinline__ bool any_wide(const uint8_t* wide, int slot) {
+  return *reinterpret_cast<const volatile uint16_t*>(wide + slot * 2) != 0;
+}
+// a + v p q, |v| zero or in [2^-32, 2^39).  Unless p q is normal, v takes one scale after the other, in the order that
+// stays in range wherever the result does.  A product beyond the largest value: the smaller scale is 1 at least, so v
+// times it does not underflow, and overflows only with the result.  A product below the normal range: one scale is
+// below 2^-63 and the other below 2^23, whose product with v is in range, or it is below 2^-126 and the result below 2^-189.
+// A zero goes first.
+__device__ __forceinline__ float add_scaled(float v, float p, float q, float a) {
+  constexpr float kLeast = 1.17549435e-38f, kLargest = 3.402823466e38f;   // normal numbers
+  const float s = p * q, mag = fabsf(s);
+  if (mag >= kLeast && mag <= kLargest) return fmaf(v, s, a);
+  const bool p_larger = fabsf(p) >= fabsf(q);
+  const float big = p_larger ? p : q, small = p_larger ? q : p;
+  return mag < kLeast && small != 0.f ? fmaf(v * big, small, a) : fmaf(v * small, big, a);
+}
+
 // Scales of a tile on their way into shared memory, four K blocks at a time; rows l, l + 32, l + 64, l + 96
 // of P are lane l's items 0 to 3, its rows of Q the items from 4 on (fp32 with one scale per 128 columns: row
 // 128 l); a warp has the items [FIRST, FIRST + NR).  The next four blocks are in flight
@@ -432,14 +459,20 @@ struct ScaleLoader {
     fence_proxy_async_smem();
     __syncwarp();
   }
-  __device__ __forceinline__ void store_rows(uint8_t* slot, uint32_t row_bytes, int lane) {
+  // wide: the slot's byte of this warp, whether one of its scales is outside the range of plain_scale
+  __device__ __forceinline__ void store_rows(uint8_t* slot, uint32_t row_bytes, uint8_t* wide, int lane) {
+    bool out = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t* d = reinterpret_cast<uint32_t*>(slot + j * row_bytes);
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+      for (int i = 0; i < NR; ++i) {
         if (FIRST + i < 4 || QROW || lane < 2) d[lane + 32 * (FIRST + i)] = v[i][j];
+        out |= !plain_scale(v[i][j]);
+      }
     }
+    out = __any_sync(0xffffffffu, out);
+    if (lane == 0) *wide = out;
     __syncwarp();
   }
 };
@@ -449,8 +482,8 @@ __device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int j) { return id
 // ------------------------------------------------------------------ pair kernel
 // What bounds it (8192 x 4096 x 7168, 481 GFLOP): UE8M0 170 us, 2.8 PFLOP/s -- the power limit, under which the SM clock
 // falls to about 1.4 GHz, and the last wave of tiles; tensor pipe busy three quarters of the cycles at 2048 rows.
-// fp32 scales 228 us, 2.1 PFLOP/s: the epilogue warps' TMEM reads and one FMA per element and K block beside the
-// MMAs.  QROW 350 us at 4096 x 7168 x 8191, 1.4 PFLOP/s: a second fp32 operation per element and the column
+// fp32 scales 227 us, 2.1 PFLOP/s: the epilogue warps' TMEM reads and one FMA per element and K block beside the
+// MMAs.  QROW 336 us at 4096 x 7168 x 8191, 1.4 PFLOP/s: a second fp32 operation per element and the column
 // scales' shared-memory reads.
 // QROW (fp32 scales only): Q's scales differ by column; otherwise one per 128 columns, and every tile
 // starts at a multiple of 128.  NC: columns of an epilogue thread; with fp32 scales bn = 2 NC, known to the
@@ -474,6 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint64_t* drain = sempty + kSfSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
+  uint8_t* wide = smem + C::misc + 8;                             // fp32 scales: [slot][scale warp]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
@@ -493,6 +527,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *reinterpret_cast<uint32_t*>(wide) = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
@@ -615,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               sf.store_atoms(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
               if (lane == 0) arrive_first(&sfull[slot]);
             } else {
-              sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, lane);
+              sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, wide + slot * 2 + warp - 2, lane);
               if (lane == 0) mbar_arrive(&sfull[slot]);
             }
             sf.load(p, KB - kb - 4);
@@ -680,60 +715,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tmem_ld<32>(t, r);
           }
         };
-        for (int kb = 0; kb < KB; ++kb) {
-          const int j4 = kb & 3;
-          if (j4 == 0) ok = wait_for(&sfull[slot], rphase, ctl, kWhereEpilogue);
-          const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + j4) * C::kRowBytes);
-          float sp[QROW ? 4 : 1];
-          if constexpr (QROW) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) sp[h] = sc[q * 32 + 8 * h + (lane >> 2)];
-          } else {
-            sp[0] = sc[q * 32 + lane] * sc[BM + (c0 >> 7)];   // bn is 128 or 256: one block of 128 columns
-          }
-          ok = ok && wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
-          ok = __all_sync(0xffffffffu, ok);
+        for (int g = 0; g < KB; g += 4) {                // groups of four K blocks, whose scales came together
+          const int end = min(g + 4, KB);
+          ok = __all_sync(0xffffffffu, wait_for(&sfull[slot], rphase, ctl, kWhereEpilogue));
           if (!ok) break;
-          tc_fence_after();
-          uint32_t r[2][32];
-          load(0, r[0]);
-          tmem_ld_wait();
+          if (any_wide(wide, slot)) {                    // 16 columns at a time
+            float sum[(NC + 31) / 32 * 32];
 #pragma unroll
-          for (int i = 0; i < (NC + 31) / 32; ++i) {
-            if (i + 1 < (NC + 31) / 32) {
-              load((i + 1) * 32, r[(i + 1) & 1]);
-            } else {                             // everything is read: the buffer may be overwritten
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) hand_back(acce0 + buf * 8);
-            }
-            const uint32_t(&v)[32] = r[i & 1];
-            float* a = acc + i * 32;
-            if constexpr (QROW) {
-              // 8 bytes of column scales serve four rows: with a row to a lane, every lane would read all
-              // columns' scales, and shared memory returns 128 bytes a clock whether they differ or not
+            for (int c = 0; c < (NC + 31) / 32 * 32; ++c) sum[c] = acc[c];
+            for (int kb = g; kb < end; ++kb) {
+              ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1));
+              if (!ok) break;
+              tc_fence_after();
+              const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + kb - g) * C::kRowBytes);
+#pragma unroll 1
+              for (int c = 0; c < NC; c += 16) {
+                const uint32_t t = t_acc + buf * acc_cols + c;
+                uint32_t r[16];
+                if constexpr (QROW) {
+                  tmem_ld_frag16(t, r);
+                  tmem_ld_frag16(t + (16u << 16), r + 8);
+                } else {
+                  tmem_ld<16>(t, r);
+                }
+                tmem_ld_wait();
+                if (c + 16 == NC) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) hand_back(acce0 + buf * 8);
+                }
 #pragma unroll
-              for (int j = 0; j < (i * 32 + 32 <= NC ? 4 : 2); ++j) {
-                const float2 sq = *reinterpret_cast<const float2*>(sc + BM + c0 + i * 32 + 8 * j + 2 * (lane & 3));
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  const int e = (h >> 1) * 16 + 4 * j + 2 * (h & 1);
-                  a[e] = fmaf(__uint_as_float(v[e]), sp[h] * sq.x, a[e]);
-                  a[e + 1] = fmaf(__uint_as_float(v[e + 1]), sp[h] * sq.y, a[e + 1]);
+                for (int i = 0; i < 16; ++i) {
+                  float sp, sq;
+                  int at;                // in sum, as the ordinary loop has its columns in acc
+                  if constexpr (QROW) {  // i = 8 (row / 16) + 4 (column / 8) + 2 (row / 8 % 2) + column % 2
+                    const int col = c + (i >> 2 & 1) * 8 + 2 * (lane & 3) + (i & 1);
+                    sp = sc[q * 32 + (i >> 3) * 16 + (i >> 1 & 1) * 8 + (lane >> 2)];
+                    sq = sc[BM + c0 + col];
+                    at = (c & ~31) + (i >> 3) * 16 + (c & 16) / 2 + (i & 7);
+                  } else {
+                    sp = sc[q * 32 + lane];
+                    sq = sc[BM + (c0 >> 7)];
+                    at = c + i;
+                  }
+                  sum[at] = add_scaled(__uint_as_float(r[i]), sp, sq, sum[at]);
                 }
               }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) a[j] = fmaf(__uint_as_float(v[j]), sp[0], a[j]);
+              if (++buf == na) { buf = 0; aphase ^= 1; }
             }
-            if (i + 1 < (NC + 31) / 32) tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < (NC + 31) / 32 * 32; ++c) acc[c] = sum[c];
+          } else {
+            for (int kb = g; kb < end; ++kb) {
+              const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + kb - g) * C::kRowBytes);
+              float sp[QROW ? 4 : 1];
+              if constexpr (QROW) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) sp[h] = sc[q * 32 + 8 * h + (lane >> 2)];
+              } else {
+                sp[0] = sc[q * 32 + lane] * sc[BM + (c0 >> 7)];   // bn is 128 or 256: one block of 128 columns
+              }
+              ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1));
+              if (!ok) break;
+              tc_fence_after();
+              uint32_t r[2][32];
+              load(0, r[0]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < (NC + 31) / 32; ++i) {
+                if (i + 1 < (NC + 31) / 32) {
+                  load((i + 1) * 32, r[(i + 1) & 1]);
+                } else {                             // everything is read: the buffer may be overwritten
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) hand_back(acce0 + buf * 8);
+                }
+                const uint32_t(&v)[32] = r[i & 1];
+                float* a = acc + i * 32;
+                if constexpr (QROW) {
+                  // 8 bytes of column scales serve four rows: with a row to a lane, every lane would read all
+                  // columns' scales, and shared memory returns 128 bytes a clock whether they differ or not
+#pragma unroll
+                  for (int j = 0; j < (i * 32 + 32 <= NC ? 4 : 2); ++j) {
+                    const float2 sq = *reinterpret_cast<const float2*>(sc + BM + c0 + i * 32 + 8 * j + 2 * (lane & 3));
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                      const int e = (h >> 1) * 16 + 4 * j + 2 * (h & 1);
+                      a[e] = fmaf(__uint_as_float(v[e]), sp[h] * sq.x, a[e]);
+                      a[e + 1] = fmaf(__uint_as_float(v[e + 1]), sp[h] * sq.y, a[e + 1]);
+                    }
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) a[j] = fmaf(__uint_as_float(v[j]), sp[0], a[j]);
+                }
+                if (i + 1 < (NC + 31) / 32) tmem_ld_wait();
+              }
+              if (++buf == na) { buf = 0; aphase ^= 1; }
+            }
           }
-          if (++buf == na) { buf = 0; aphase ^= 1; }
-          if (j4 == 3 || kb == KB - 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sempty[slot]);
-            if (++slot == kSfSlots) { slot = 0; rphase ^= 1; }
-          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+          if (++slot == kSfSlots) { slot = 0; rphase ^= 1; }
         }
         if (!ok) break;
       }
@@ -782,6 +866,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   uint64_t* drain = sempty + kSfSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
+  uint8_t* wide = smem + C::misc + 8;                             // fp32 scales: [slot][scale warp]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl ctl{abort_flag, p.status, p.timeout_ns};
 
@@ -800,6 +885,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *reinterpret_cast<uint32_t*>(wide) = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
@@ -905,7 +991,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         if constexpr (MX)
           sf.store_atoms(smem + C::sfp + slot * 512, smem + C::sfq + slot * C::kSfq, lane);
         else
-          sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, lane);
+          sf.store_rows(smem + C::ring + slot * 4 * C::kRowBytes, C::kRowBytes, wide + slot * 2, lane);
         if (lane == 0) mbar_arrive(&sfull[slot]);
         sf.load(p, kb1 - kb - 4);
         if (++slot == kSfSlots) { slot = 0; phase ^= 1; }
@@ -938,40 +1024,71 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       } else {
 #pragma unroll
         for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const int j4 = (kb - kb0) & 3;
-          if (j4 == 0) ok = wait_for(&sfull[slot], rphase, ctl, kWhereEpilogue);
-          ok = ok && wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1);
-          ok = __all_sync(0xffffffffu, ok);
+        for (int g = kb0; g < kb1; g += 4) {             // groups of four K blocks, whose scales came together
+          const int end = min(g + 4, kb1);
+          ok = __all_sync(0xffffffffu, wait_for(&sfull[slot], rphase, ctl, kWhereEpilogue));
           if (!ok) break;
-          tc_fence_after();
-          const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + j4) * C::kRowBytes);
-          const float sp = sc[q * 32 + lane];
+          if (any_wide(wide, slot)) {                    // 8 columns at a time
+            float sum[COLS];
 #pragma unroll
-          for (int c = 0; c < COLS; c += CH) {
-            uint32_t r[CH];
-            tmem_ld<CH>(t_acc + buf * BN + c, r);
-            tmem_ld_wait();
-            if (c + CH == COLS) {      // everything is read: the buffer may be overwritten
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&acce[buf]);
+            for (int c = 0; c < COLS; ++c) sum[c] = acc[c];
+            for (int kb = g; kb < end; ++kb) {
+              ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1));
+              if (!ok) break;
+              tc_fence_after();
+              const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + kb - g) * C::kRowBytes);
+              const float sp = sc[q * 32 + lane];
+#pragma unroll 1
+              for (int c = 0; c < COLS; c += 8) {
+                uint32_t r[8];
+                tmem_ld<8>(t_acc + buf * BN + c, r);
+                tmem_ld_wait();
+                if (c + 8 == COLS) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&acce[buf]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  sum[c + i] = add_scaled(__uint_as_float(r[i]), sp, sc[BM + half * COLS + c + i], sum[c + i]);
+              }
+              if (++buf == NA) { buf = 0; aphase ^= 1; }
             }
 #pragma unroll
-            for (int j = 0; j < CH; j += 4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(sc + BM + half * COLS + c + j);
-              acc[c + j] += __uint_as_float(r[j]) * (sp * s4.x);
-              acc[c + j + 1] += __uint_as_float(r[j + 1]) * (sp * s4.y);
-              acc[c + j + 2] += __uint_as_float(r[j + 2]) * (sp * s4.z);
-              acc[c + j + 3] += __uint_as_float(r[j + 3]) * (sp * s4.w);
+            for (int c = 0; c < COLS; ++c) acc[c] = sum[c];
+          } else {
+            for (int kb = g; kb < end; ++kb) {
+              ok = __all_sync(0xffffffffu, wait_for(&accf[buf], aphase, ctl, kWhereEpilogue + 1));
+              if (!ok) break;
+              tc_fence_after();
+              const float* sc = reinterpret_cast<const float*>(smem + C::ring + (slot * 4 + kb - g) * C::kRowBytes);
+              const float sp = sc[q * 32 + lane];
+#pragma unroll
+              for (int c = 0; c < COLS; c += CH) {
+                uint32_t r[CH];
+                tmem_ld<CH>(t_acc + buf * BN + c, r);
+                tmem_ld_wait();
+                if (c + CH == COLS) {      // everything is read: the buffer may be overwritten
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&acce[buf]);
+                }
+#pragma unroll
+                for (int j = 0; j < CH; j += 4) {
+                  const float4 s4 = *reinterpret_cast<const float4*>(sc + BM + half * COLS + c + j);
+                  acc[c + j] += __uint_as_float(r[j]) * (sp * s4.x);
+                  acc[c + j + 1] += __uint_as_float(r[j + 1]) * (sp * s4.y);
+                  acc[c + j + 2] += __uint_as_float(r[j + 2]) * (sp * s4.z);
+                  acc[c + j + 3] += __uint_as_float(r[j + 3]) * (sp * s4.w);
+                }
+              }
+              if (++buf == NA) { buf = 0; aphase ^= 1; }
             }
           }
-          if (++buf == NA) { buf = 0; aphase ^= 1; }
-          if (j4 == 3 || kb == kb1 - 1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sempty[slot]);
-            if (++slot == kSfSlots) { slot = 0; rphase ^= 1; }
-          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+          if (++slot == kSfSlots) { slot = 0; rphase ^= 1; }
         }
         if (!ok) break;
       }

@@ -388,8 +388,8 @@ int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_type, int bl
  * consecutive rows next to each other (row stride 1) load fastest.  out [M][N], row pitch ldo, is
  * bf16 or fp32 (out_type); accumulate (fp32 only) adds to it, one addition per element and call (sums
  * below 2^-126 may become 0).  Products and sums are fp32 on the tensor
- * cores: UE8M0 scales are applied by the block-scaled MMA, fp32 scales (any finite value) to each K
- * block's fp32 sum outside it.  0 <= M, N <= 2^30, 0 <= K <= 2^28, odd ones included; K == 0 gives
+ * cores: UE8M0 scales are applied by the block-scaled MMA, fp32 scales (any finite value, also where sA sB by
+ * itself is out of fp32's range) to each K block's fp32 sum outside it.  0 <= M, N <= 2^30, 0 <= K <= 2^28, odd ones included; K == 0 gives
  * zeros (or adds nothing).
  * A and B 16-byte aligned, lda and ldb multiples of 16 (one row: any pitch); out aligned to its type (16
  * bytes and a pitch of a multiple of 16 bytes store fastest); out may not overlap the operands.
