@@ -188,11 +188,16 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const W
   return true;
 }
 // Arrivals on the same barrier of CTA 0 of the pair.  A release at cluster scope costs a memory barrier of
-// about 0.7 us, more than a K block's MMAs.  arrive_first hands scale atoms over: each is read by the async
-// proxy of the SM that wrote it, which the writer's proxy fence has shown it to.  hand_back returns an
+// about 0.7 us, more than a K block's MMAs (8192 x 4096 x 7168: 208 us instead of 168).  arrive_first hands scale atoms in
+// this CTA's shared memory over, to be copied to TMEM by CTA 0's thread after see_first: a release and an acquire between
+// the CTAs of the cluster that are restricted to shared memory, at no measurable cost.  hand_back returns an
 // accumulator: tcgen05.fence::before_thread_sync orders the loads from it, no other memory is passed on.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+               "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
+__device__ __forceinline__ void see_first() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 __device__ __forceinline__ void hand_back(uint32_t bar_cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
@@ -600,6 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if ((!MX || kb == 0) && !wait_for(&acce[buf], aphase ^ 1, ctl, kWhereMma)) { ok = false; break; }
             if (MX && (kb & 3) == 0) {
               if (!wait_for(&sfull[sf], sphase, ctl, kWhereMma + 2)) { ok = false; break; }
+              see_first();
               tc_fence_after();
               tsp = tmem + sf_col + sf * 16;     // the slots' columns alternate as well
               const uint64_t sp = sp0 + sf * (512 >> 4), sq = sq0 + sf * (C::kSfq >> 4);
