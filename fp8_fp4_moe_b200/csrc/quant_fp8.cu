@@ -411,6 +411,12 @@ cudaError_t launch_fmt(const QuantArgs& a, int fmt, bool tile, cudaStream_t s, i
 }
 
 bool aligned(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether scales of `rows` x `blocks` have a place each: the strides of one index step over all of the other.
+bool distinct(long long rows, long long row_stride, long long blocks, long long block_stride) {
+  if (row_stride < 0 || block_stride < 0 || (rows > 1 && row_stride == 0) || (blocks > 1 && block_stride == 0)) return false;
+  return rows == 1 || blocks == 1 || (row_stride - 1) / (blocks - 1) >= block_stride ||
+         (block_stride - 1) / (rows - 1) >= row_stride;
+}
 
 }  // namespace
 
@@ -427,14 +433,15 @@ extern "C" int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_t
   if (q == nullptr && qt == nullptr) return MOE_ERR_INVALID_ARG;
   const uintptr_t esize = x_type == MOE_TYPE_FP32 ? 4 : 2, ssize = scale_type == MOE_SCALE_FP32 ? 4 : 1;
   if (!aligned(x, esize) || (M > 1 && ldx < K)) return MOE_ERR_INVALID_ARG;
-  if (q && (!aligned(q, 16) || !aligned(scales, ssize) || (M > 1 && (ldq < K || ldq % 16)) || s_row_stride < 0 ||
-            s_block_stride < 0))
+  const int mb = (M + 127) / 128, kb = (K + 127) / 128;
+  const bool tiles = block == MOE_BLOCK_TILE;
+  if ((tiles || qt) && mb > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (q && (!aligned(q, 16) || !aligned(scales, ssize) || (M > 1 && (ldq < K || ldq % 16)) ||
+            !distinct(tiles ? mb : M, s_row_stride, kb, s_block_stride)))
     return MOE_ERR_INVALID_ARG;
   if (qt && (!aligned(qt, 16) || !aligned(scales_t, ssize) || (K > 1 && (ldqt < M || ldqt % 16)) ||
-             st_row_stride < 0 || st_block_stride < 0))
+             !distinct(tiles ? kb : K, st_row_stride, mb, st_block_stride)))
     return MOE_ERR_INVALID_ARG;
-  const int mb = (M + 127) / 128;
-  if ((block == MOE_BLOCK_TILE || qt) && mb > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
   int dev = -1, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -456,10 +463,9 @@ extern "C" int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_t
   a.st_blk = st_block_stride;
   a.ue8m0 = scale_type == MOE_SCALE_UE8M0;
   a.x_vec = aligned(x, 16) && (M == 1 || ldx * (long long)esize % 16 == 0);
-  const bool tile = block == MOE_BLOCK_TILE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = x_type == MOE_TYPE_BF16   ? launch_fmt<__nv_bfloat16>(a, format, tile, s, sms)
-                  : x_type == MOE_TYPE_FP16 ? launch_fmt<__half>(a, format, tile, s, sms)
-                                            : launch_fmt<float>(a, format, tile, s, sms);
+  cudaError_t e = x_type == MOE_TYPE_BF16   ? launch_fmt<__nv_bfloat16>(a, format, tiles, s, sms)
+                  : x_type == MOE_TYPE_FP16 ? launch_fmt<__half>(a, format, tiles, s, sms)
+                                            : launch_fmt<float>(a, format, tiles, s, sms);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

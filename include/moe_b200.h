@@ -367,14 +367,15 @@ enum moe_block {
  *       scale of row r (row block r / 128) and K block b at scales[r * s_row_stride + b * s_block_stride]
  *   qt  [K][M], row pitch ldqt: the transposed copy, blocks of 128 along M or 128 x 128; scale of
  *       column c (column block) and row block b at scales_t[c * st_row_stride + b * st_block_stride]
- * either may be NULL (with its scales), not both.  Per block: p = the smallest integer >= -126 with
+ * either may be NULL (with its scales), not both.  Scales have a place each: one stride steps over all
+ * of the other index.  Per block: p = the smallest integer >= -126 with
  * amax <= MAX * 2^p, MAX = 448 (E4M3) or 57344 (E5M2); p = 0 for an all-zero block; the codes are
  * x * 2^-p rounded to nearest even, scale = 2^p (UE8M0 code p + 127).  A NaN becomes a NaN code and does
  * not count towards amax; an infinity gives its block the largest scale, in which it becomes +-MAX and
  * the finite values of the block zeros or small codes.  The last block of a row or column may be short.
  * M == 0 or K == 0 writes nothing.  Only the K (M) codes of a row are written, not its padding.
  * x, 16-byte aligned q and qt with pitches a multiple of 16 (one row: any pitch).  x may not overlap the
- * outputs.  Asynchronous on `stream`.  MOE_OK, MOE_ERR_INVALID_ARG (pointer, pitch, type),
+ * outputs.  Asynchronous on `stream`.  MOE_OK, MOE_ERR_INVALID_ARG (pointer, pitch, stride, type),
  * MOE_ERR_UNSUPPORTED_SHAPE (negative; over 2^30; over 8,388,480 rows with tiles or qt) or MOE_ERR_CUDA. */
 int moe_quant_fp8(int M, int K, const void* x, long long ldx, int x_type, int block, int format, int scale_type,
                   void* q, long long ldq, void* scales, long long s_row_stride, long long s_block_stride, void* qt,
