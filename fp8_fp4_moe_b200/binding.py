@@ -234,8 +234,8 @@ def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, 
     along K, and its scales s [M or ceil(M/128), ceil(K/128)]; with `cols`: the transposed copy qt [K, M],
     blocked along M, and st [K or ceil(K/128), ceil(M/128)]; None for what is not asked for.  Scales are
     fp32 or (scale_dtype torch.uint8) UE8M0 codes, stored so that those of consecutive rows are adjacent,
-    and row pitches of the codes are multiples of 16: what gemm_fp8 takes.  `out`: the four to write, scales of any strides that give
-    each a place of its own."""
+    and row pitches of the codes are multiples of 16: what gemm_fp8 takes.  `out`: the four to write,
+    scales of any strides that give each a place of its own."""
     q, s, qt, st = (None, None, None, None) if out is None else out
     return _call("quant_fp8", stream, x, x, _choice("block", block, "row", "tile"), rows, cols, dtype, scale_dtype,
                  q, s, qt, st)
