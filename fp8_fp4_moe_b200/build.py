@@ -14,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +24,7 @@ LIB = os.path.join(PKG, "libmoe_b200.so")
 OPS = os.path.join(PKG, "_moe_ops.so")
 OPS_SOURCE = "ops_binding.cpp"
 BUILD_DIR = os.path.join(ROOT, "_build")
+OPS_STAMP = os.path.join(BUILD_DIR, "_moe_ops.txt")
 SOURCES = ["gemm_sm100.cu", "path_kernels.cu", "moe_api.cu", "noalloc.cu", "dense_api.cu", "gemm_fp8.cu", "quant_fp8.cu",
            "balance.cu"]
 HEADERS = ["common.cuh", "kernels.h", "path_phases.cuh"]
@@ -79,15 +81,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _built_for() -> str:
+    """The interpreter and torch whose C++ interface _moe_ops.so is compiled against."""
+    import torch
+    return f"Python {sys.version}, torch {torch.__version__} at {os.path.dirname(torch.__file__)}"
+
+
+def ops_stale() -> bool:
+    """Whether _moe_ops.so is missing, older than its sources, or built for another interpreter or torch."""
+    if _stale(OPS, [os.path.join(CSRC, OPS_SOURCE), os.path.join(INCLUDE, "moe_b200.h")]):
+        return True
+    if not os.path.exists(OPS_STAMP):
+        return True
+    with open(OPS_STAMP) as f:
+        return f.read() != _built_for()
+
+
 def build_ops(force: bool = False, verbose: bool = False) -> str:
     """Compile the native part of the binding; it finds libmoe_b200.so beside itself, torch's libraries in
     the process that imported torch."""
-    import sysconfig
-
     import torch
-    src = os.path.join(CSRC, OPS_SOURCE)
-    if not force and not _stale(OPS, [src, os.path.join(INCLUDE, "moe_b200.h")]):
+    if not force and not ops_stale():
         return OPS
+    src = os.path.join(CSRC, OPS_SOURCE)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     at = os.path.dirname(torch.__file__)
     inc = ["-I" + p for p in [INCLUDE, sysconfig.get_path("include"), os.path.join(cuda, "include"),
@@ -101,6 +117,9 @@ def build_ops(force: bool = False, verbose: bool = False) -> str:
         sys.stderr.write(r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed: {' '.join(cmd)}")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(OPS_STAMP, "w") as f:
+        f.write(_built_for())
     return OPS
 
 
