@@ -15,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -77,8 +78,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
-    build_ops(force, verbose)
+    missing = ops_prerequisites()
+    if missing:   # the library is complete without it; the functions that need it say so when they are called
+        warnings.warn(f"{os.path.basename(OPS)} not built, missing: {', '.join(missing)}")
+    else:
+        build_ops(force, verbose)
     return LIB
+
+
+def ops_prerequisites() -> list:
+    """What the native part of the binding needs and this machine lacks."""
+    try:
+        import torch
+    except ImportError:
+        return ["torch"]
+    need = [os.path.join(sysconfig.get_path("include"), "Python.h"),
+            os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "autograd", "python_variable.h")]
+    return [p for p in need if not os.path.exists(p)] + ([] if shutil.which("g++") else ["g++"])
 
 
 def _built_for() -> str:
