@@ -233,9 +233,10 @@ def quant_fp8(x, block="row", rows=True, cols=False, dtype=torch.float8_e4m3fn, 
     Returns (q, s, qt, st).  With `rows`: q [M, K] of `dtype` (float8_e4m3fn or float8_e5m2), blocked
     along K, and its scales s [M or ceil(M/128), ceil(K/128)]; with `cols`: the transposed copy qt [K, M],
     blocked along M, and st [K or ceil(K/128), ceil(M/128)]; None for what is not asked for.  Scales are
-    fp32 or (scale_dtype torch.uint8) UE8M0 codes, stored so that those of consecutive rows are adjacent,
-    and row pitches of the codes are multiples of 16: what gemm_fp8 takes.  `out`: the four to write,
-    scales of any strides that give each a place of its own."""
+    fp32 or (scale_dtype torch.uint8) UE8M0 codes, the same powers of two in either; for many rows gemm_fp8 is faster
+    with UE8M0 (a weight gradient takes little more than half the time).  They are stored so that those of
+    consecutive rows are adjacent, and row pitches of the codes are multiples of 16: what gemm_fp8 takes.
+    `out`: the four to write, scales of any strides that give each a place of its own."""
     q, s, qt, st = (None, None, None, None) if out is None else out
     return _call("quant_fp8", stream, x, x, _choice("block", block, "row", "tile"), rows, cols, dtype, scale_dtype,
                  q, s, qt, st)
@@ -246,15 +247,18 @@ def gemm_fp8(A, A_scales, B, B_scales, out=None, out_dtype=torch.bfloat16, accum
     """Block-scaled FP8 product through moe_gemm_fp8: out [M, N] (bf16 or fp32) = A . B^T, or out += A . B^T
     (`accumulate`, fp32 `out`).  A [M, K], B [N, K]: float8_e4m3fn or float8_e5m2 codes (uint8: E4M3), rows
     contiguous with pitches a multiple of 16 bytes; scales fp32 or uint8 (UE8M0), both alike, [rows,
-    ceil(K/128)] or, one per 128 rows, [ceil(rows/128), ceil(K/128)], of any strides.  Returns (out,
-    workspace); the first int32 of the workspace is the device status once the stream has run the call."""
+    ceil(K/128)] or, one per 128 rows, [ceil(rows/128), ceil(K/128)], of any strides.  The tensor cores apply
+    UE8M0 scales; fp32 scales (any finite value) are applied by fp32 additions beside them, which for many rows
+    take 1.3 times as long, 1.8 times with one scale per row of B.  Returns (out, workspace); the first int32 of the workspace is the device status once the stream has run the call."""
     return _call("gemm_fp8", stream, A, A, A_scales, B, B_scales, out, out_dtype, accumulate, workspace)
 
 
 def balance_loss(logits, topk_ids, coef=1.0, offsets=None, mask=None, score="softmax", workspace=None, stream=None):
     """Balance loss of the router through moe_balance_loss: logits [T, E] (fp32 or bf16), topk_ids int32
     [T, k], optionally offsets int32 [S + 1] of packed sequences and mask bool [T] of the tokens that count.
-    Returns (loss fp32 [], counts int32 [S, E], probs fp32 [S, E], tokens int32 [S])."""
+    Returns (loss fp32 [], counts int32 [S, E], probs fp32 [S, E], tokens int32 [S]).  No autograd function: the
+    loss is detached from logits that require a gradient, which balance_loss_backward computes.  The logits are
+    the router's products x W_router^T of all experts, without the selection bias."""
     return _call("balance_loss", stream, logits, logits, topk_ids, coef, offsets, mask,
                  _choice("score", score, "softmax", "sigmoid"), workspace)
 

@@ -8,10 +8,10 @@
 // The loss reads the logits once; the gradient needs the counts of all tokens, so it reads them again.
 // Sums over tokens run in a fixed order (per warp, per block, then over blocks), so results repeat bit
 // for bit; counts are integers.
-// T = 32768, E = 256 fp32, loss and gradient: 30.8 us for 101 MB (3.3 TB/s).  An exponential, its share of two
-// shuffled reductions and two to four fp32 operations per logit, with 16 warps an SM (registers: a row's logits, the
-// next row's on their way and the sums or counts), bound it before memory does.  T = 512: 11.2 us, two
-// launches and their latencies.
+// T = 32768, E = 256 fp32, loss and gradient: 29.4 us for 101 MB (3.4 TB/s).  Latency bounds it: a row's logits, the
+// next row's on their way and the sums or counts take all 128 registers (up to 172 bytes a thread are spilled beyond 128
+// experts), which leaves 16 warps an SM; an instruction issues in 45 to 51 % of the cycles, and what a warp waits for most is
+// memory.  A block's 3.5 rounds of tokens take four.  T = 512: 10.6 us, two launches and their latencies.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -684,7 +684,7 @@ cudaError_t launch_as(BalanceArgs& a, bool grad, cudaStream_t s) {
   // launches 8.5).  Several: a block of the two
   // launches takes about 4 us for each sequence of its chunk, one after the other; clusters take 5 us and 0.135 us
   // for each sequence over what fits the SMs (T = 16, S = 57: 79 us by chunks; T = 8191, S = 13: 22 us by chunks, 25
-  // by clusters).
+  // by clusters; 22.5 the whole step).
   a.clusters = a.S == 1 ? a.T <= kCluster * round * kClusterRounds
                         : 4.0 * a.chunk * a.S / a.T > 5.0 + 0.135 * a.S;
   return a.clusters

@@ -488,8 +488,10 @@ __device__ __forceinline__ uint32_t with_byte(uint32_t idesc, int j) { return id
 // What bounds it (8192 x 4096 x 7168, 481 GFLOP): UE8M0 170 us, 2.8 PFLOP/s -- the power limit, under which the SM clock
 // falls to about 1.4 GHz, and the last wave of tiles; tensor pipe busy three quarters of the cycles at 2048 rows.
 // fp32 scales 227 us, 2.1 PFLOP/s: the epilogue warps' TMEM reads and one FMA per element and K block beside the
-// MMAs.  QROW 336 us at 4096 x 7168 x 8191, 1.4 PFLOP/s: a second fp32 operation per element and the column
-// scales' shared-memory reads.
+// MMAs.  No unit is full (2048 rows: tensor pipe 51 %, FMA pipe 30 %, issue slots 48 %): buffers go back and
+// forth between MMAs and additions, two of 256 columns, and each side waits for the other.  QROW 336 us at 4096 x 7168 x
+// 8191, 1.4 PFLOP/s: a second fp32 operation per element and the column scales' shared-memory reads (tensor pipe 33 %, FMA
+// pipe 37 %, issue slots 54 %).
 // QROW (fp32 scales only): Q's scales differ by column; otherwise one per 128 columns, and every tile
 // starts at a multiple of 128.  NC: columns of an epilogue thread; with fp32 scales bn = 2 NC, known to the
 // compiler so that it can move loads and additions of different columns past each other (NC = 112: the
@@ -1274,8 +1276,8 @@ Cut choose(int M, int N, int KB, int sms, bool qrow, bool mx) {
   }
   if (!swap)
     for (int bn = 256; bn >= 64; bn -= 32) {
-      // the widths compiled for fp32 scales.  224, column scales: 4096 x 7168 x 8191 is 512 tiles, 6.9 waves, 350 us; with
-      // 256 columns 448 tiles in 6.05 waves, 366 us.  Scales per 128 columns need tiles that start with them
+      // the widths compiled for fp32 scales.  224, column scales: 4096 x 7168 x 8191 is 512 tiles, 6.9 waves, 338 us; with
+      // 256 columns 448 tiles in 6.05 waves, 361 us.  Scales per 128 columns need tiles that start with them
       if (!mx && bn != 256 && bn != 128 && !(qrow && bn == 224)) continue;
       const double waves = (double)up((long)up(M, 256) * up(N, bn), sms / 2);
       const double block = mx ? 0.130 + 0.00124 * bn : qrow ? 0.231 + 0.0023 * bn : 0.131 + 0.00172 * bn;
