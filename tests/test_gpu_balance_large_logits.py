@@ -81,3 +81,32 @@ def test_a_masked_out_row_is_even(cuda_lib, score, fill):
     loss, counts, probs, tokens = binding.balance_loss(l.cuda(), ids.cuda(), offsets=off, score=score)
     assert torch.isfinite(loss) and torch.isfinite(probs).all()
     assert ((probs[1] - 1 / 64).abs() <= 114 * U / 64).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_captured_step_follows_its_logits(cuda_lib, score):
+    # ordinary rows in one replay, rows far from zero in the next; padding behind the last sequence stays zero
+    E, k = 48, 2
+    far = _rows(E, torch.float32)
+    T = far.shape[0]
+    near = torch.randn(T, E, generator=torch.Generator().manual_seed(3))
+    l, ids = near.cuda(), (torch.arange(T * k).reshape(T, k) * 7 % E).to(torch.int32).cuda()
+    off = torch.tensor([0, 9, 9, T - 3], dtype=torch.int32, device="cuda")
+    one = torch.ones((), device="cuda")
+
+    def step():
+        r = binding.balance_loss(l, ids, offsets=off, score=score)
+        return (*r, binding.balance_loss_backward(one, l, r[1], r[3], k, offsets=off, score=score))
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for src in (near, far, near):
+        l.copy_(src)
+        g.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert all(torch.isfinite(x.float()).all() for x in got) and (got[4][-3:] == 0).all()

@@ -105,3 +105,41 @@ def test_ue8m0_scales_that_cancel_and_zeros_under_large_ones(cuda_lib, M, N, K):
     out, ws = binding.gemm_fp8(A, f(sa), B, f(sb), out_dtype=torch.float32)
     x, y = O.dequant(a, np.exp2(sa.astype(float))), O.dequant(b, np.exp2(sb.astype(float)))
     _compare(out, ws, (torch.from_numpy(x).cuda() @ torch.from_numpy(y).cuda().T).cpu().numpy(), K)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 200, 1300), (300, 700, 1300), (300, 5888, 640)])
+@pytest.mark.parametrize("b_per", ["row", "tile"])
+def test_captured_products_at_once_follow_their_scales(cuda_lib, M, N, K, b_per):
+    # two streams in one graph, accumulated and not; scales that are ordinary in one replay and extreme in the next
+    rng = np.random.default_rng(N)
+    a, sa, A = _operand(rng, M, K, [0, 1], "row", False)
+    b, sb, B = _operand(rng, N, K, [0, 1], b_per, False)
+    f = lambda e: torch.from_numpy(np.exp2(e.astype(np.float64)).astype(np.float32)).cuda()   # noqa: E731
+    As, Bs, acc = f(sa), f(sb), torch.zeros(M, N, device="cuda")
+    As2, Bs2 = As.clone(), Bs.clone()
+    side = torch.cuda.Stream()
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            acc.zero_()
+            binding.gemm_fp8(A, As2, B, Bs2, out=acc, accumulate=True)
+        r = binding.gemm_fp8(A, As, B, Bs, out_dtype=torch.float32)
+        torch.cuda.current_stream().wait_stream(side)
+        return r
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, ws = step()
+    kb = O.blocks(K)
+    for shift in ([0] * kb, [100] * kb, rng.choice([0, 0, 90, -110], kb), [-120] * kb, [0] * kb):
+        e, e2 = np.asarray(shift), -np.asarray(shift)[::-1]
+        As.copy_(f(sa + e)), Bs.copy_(f(sb - e))
+        As2.copy_(f(sa + e2)), Bs2.copy_(f(sb - e2))
+        g.replay()
+        x, y = O.dequant(a, np.exp2(sa.astype(float))), O.dequant(b, np.exp2(sb.astype(float)))
+        ref = (torch.from_numpy(x).cuda() @ torch.from_numpy(y).cuda().T).cpu().numpy()
+        _compare(out, ws, ref, K)
+        _compare(acc, ws, ref, K)
